@@ -18,19 +18,31 @@ __all__ = ["fa_fwd", "fa_fwd_f16", "fa_fwd_bf16", "fa_status_string",
            "fa_fwd_splitkv", "fa_splitkv_workspace_size", "fa_splitkv_launches", "fa_split_plan",
            "fa_fwd_gqa", "fa_fwd_gqa_splitkv", "fa_fwd_varlen", "attention_forward_varlen",
            "fa_fwd_local", "fa_fwd_dropout",
+           "KV4_GROUP", "kv4_empty_cache", "kv4_write", "kv4_read", "kv4_attention", "rotary",
+           "rotary_frequencies",
            "FaError", "library", "EXPORTED_SYMBOLS", "FA_F16", "FA_BF16"]
 
 (FA_OK, FA_ERR_INVALID_ARG, FA_ERR_UNSUPPORTED, FA_ERR_CUDA, FA_ERR_TIMEOUT,
- FA_ERR_BAD_SEQLENS, FA_ERR_DEVICE_CHECK) = range(7)
+ FA_ERR_BAD_SEQLENS, FA_ERR_DEVICE_CHECK, FA_ERR_BAD_PAGES, FA_ERR_BAD_AXIS) = range(9)
 FA_F16, FA_BF16 = 0, 1
 
 EXPORTED_SYMBOLS = ("fa_fwd", "fa_fwd_f16", "fa_fwd_bf16", "fa_status_string",
                     "fa_device_status", "fa_last_device_status", "fa_splitkv_workspace_size",
                     "fa_splitkv_launches", "fa_fwd_splitkv", "fa_fwd_gqa", "fa_fwd_gqa_splitkv",
                     "fa_fwd_varlen", "fa_fwd_local", "fa_selftest_timeout", "fa_fwd_dropout",
-                    "fa_split_plan")
+                    "fa_split_plan", "fa_kv4_write", "fa_kv4_read", "fa_kv4_attention",
+                    "fa_kv4_attention_workspace_size", "fa_rotary")
 
 _LIB = None
+
+
+class Kv4Cache(ctypes.Structure):
+    """fa_kv4_cache_t."""
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p),
+                ("page_table", ctypes.c_void_p), ("seq_lens", ctypes.c_void_p),
+                ("cu_seqlens", ctypes.c_void_p), ("B", ctypes.c_int), ("max_seqlen", ctypes.c_int),
+                ("total", ctypes.c_int), ("pages", ctypes.c_int), ("max_pages", ctypes.c_int),
+                ("page_size", ctypes.c_int), ("H_kv", ctypes.c_int), ("D", ctypes.c_int)]
 
 
 class FaError(RuntimeError):
@@ -104,6 +116,19 @@ def _declare(lib: ctypes.CDLL) -> ctypes.CDLL:
                                    ctypes.c_ulonglong, f, i, vp]
     lib.fa_fwd_dropout.restype = i
     lib.fa_selftest_timeout.restype = i
+    # cache, K, V, k_strides, v_strides, K_out, V_out, dtype, stream
+    cache, ll3 = ctypes.POINTER(Kv4Cache), ctypes.POINTER(ctypes.c_longlong)
+    lib.fa_kv4_write.argtypes = [cache, vp, vp, ll3, ll3, vp, vp, i, vp]
+    lib.fa_kv4_read.argtypes = [cache, vp, vp, i, vp]
+    lib.fa_kv4_attention_workspace_size.argtypes = [cache, i, i, ctypes.POINTER(ctypes.c_size_t)]
+    # cache, Q, q_strides, O, LSE, H, window_left, scale, dtype, workspace, bytes, stream
+    lib.fa_kv4_attention.argtypes = [cache, vp, ll3, vp, vp, i, i, f, i, vp, ctypes.c_size_t, vp]
+    # X, strides, Y, strides, H, twice; positions, inv_freq, axes, T, n_axes, n_freq, D,
+    # interleaved, inverse, dtype, stream
+    lib.fa_rotary.argtypes = [vp, ll3, vp, ll3, i, vp, ll3, vp, ll3, i, vp, vp, vp, i, i, i, i, i, i, i, vp]
+    for fn in (lib.fa_kv4_write, lib.fa_kv4_read, lib.fa_kv4_attention_workspace_size,
+               lib.fa_kv4_attention, lib.fa_rotary):
+        fn.restype = i
     return lib
 
 
@@ -384,3 +409,7 @@ def attention_forward_varlen(q, k, v, cu_seqlens, max_seqlen: int, causal: bool 
     if rc != FA_OK:
         raise FaError(rc, "fa_fwd_varlen")
     return out, lse
+
+
+from .cache import (KV4_GROUP, kv4_attention, kv4_empty_cache, kv4_read, kv4_write, rotary,  # noqa: E402
+                    rotary_frequencies)

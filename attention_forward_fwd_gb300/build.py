@@ -1,6 +1,6 @@
 """Builds libfa_gb300.so in-tree with nvcc for sm_103a.
 
-The library has one translation unit (``csrc/fa_api.cu``); the ptxas
+The library's translation units (``UNITS``) compile side by side; the ptxas
 resource report of the last build is kept in ``_build/ptxas.txt`` at the
 repository root.
 """
@@ -10,6 +10,7 @@ import os
 import re
 import shutil
 import subprocess
+import tempfile
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG_DIR)
@@ -21,6 +22,7 @@ LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
 DEBUG_LIB_PATH = os.path.join(PKG_DIR, "libfa_gb300_debug.so")
 DEBUG_FLAGS = ["-DFA_DEBUG=1"]
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
+UNITS = ("fa_api.cu", "fa_kv4.cu")
 COMPILE_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-shared", "-Xcompiler", "-fPIC"]
 
 
@@ -119,15 +121,32 @@ def build(force: bool = False, verbose: bool = False, debug: bool = False) -> st
     os.makedirs(out_dir, exist_ok=True)
     tmp = lib + ".tmp"
     stamp = source_hash(debug)
-    cmd = [_nvcc(), *ARCH_FLAGS, *COMPILE_FLAGS, *(DEBUG_FLAGS if debug else []), "-Xptxas", "-v",
-           "-I", INCLUDE, "-o", tmp, os.path.join(CSRC, "fa_api.cu")]
-    res = subprocess.run(cmd, capture_output=True, text=True)
+    compile_flags = [f for f in COMPILE_FLAGS if f != "-shared"]
+    objs, cmds = [], []
+    for unit in UNITS:
+        objs.append(os.path.join(out_dir, unit + (".debug.o" if debug else ".o")))
+        cmds.append([_nvcc(), *ARCH_FLAGS, *compile_flags, *(DEBUG_FLAGS if debug else []), "-Xptxas", "-v",
+                     "-I", INCLUDE, "-c", "-o", objs[-1], os.path.join(CSRC, unit)])
+    outs = [tempfile.TemporaryFile("w+") for _ in cmds]
+    runs = [subprocess.Popen(cmd, stdout=out, stderr=subprocess.STDOUT) for cmd, out in zip(cmds, outs)]
+    logs = []
+    for run, out in zip(runs, outs):
+        run.wait()
+        out.seek(0)
+        logs.append(out.read())
+        out.close()
     with open(os.path.join(out_dir, "ptxas_debug.txt" if debug else "ptxas.txt"), "w") as f:
-        f.write(" ".join(cmd) + "\n" + res.stdout + res.stderr)
-    if res.returncode != 0:
-        raise RuntimeError(f"nvcc failed ({res.returncode}):\n{res.stderr[-4000:]}")
+        for cmd, log in zip(cmds, logs):
+            f.write(" ".join(cmd) + "\n" + log)
+    for run, log in zip(runs, logs):
+        if run.returncode != 0:
+            raise RuntimeError(f"nvcc failed ({run.returncode}):\n{log[-4000:]}")
+    link = subprocess.run([_nvcc(), *ARCH_FLAGS, "-shared", "-Xcompiler", "-fPIC", "-o", tmp, *objs],
+                          capture_output=True, text=True)
+    if link.returncode != 0:
+        raise RuntimeError(f"nvcc failed to link ({link.returncode}):\n{link.stderr[-4000:]}")
     try:
-        check_launch_registers(res.stdout + res.stderr)
+        check_launch_registers("".join(logs))
     except RuntimeError:
         os.remove(tmp)
         raise
@@ -135,7 +154,7 @@ def build(force: bool = False, verbose: bool = False, debug: bool = False) -> st
     with open(lib + ".sha256", "w") as f:
         f.write(stamp + "\n")
     if verbose:
-        print(res.stderr)
+        print("".join(logs))
     return lib
 
 

@@ -13,6 +13,7 @@
 #include "fa_fwd_kernel.cuh"
 #include "fa_fwd_wide.cuh"
 #include "fa_gb300.h"
+#include "fa_kv4_status.h"
 
 namespace {
 
@@ -745,13 +746,15 @@ const char* fa_status_string(int status) {
         case FA_ERR_TIMEOUT: return "a device-side wait timed out";
         case FA_ERR_BAD_SEQLENS: return "a sequence offset was out of range (that sequence was skipped)";
         case FA_ERR_DEVICE_CHECK: return "a device-side invariant check failed (debug build)";
+        case FA_ERR_BAD_PAGES: return "a sequence length or page number lay outside the quantised cache";
+        case FA_ERR_BAD_AXIS: return "a rotary frequency named an axis that the positions do not have";
         default: return "unknown status";
     }
 }
 
 int fa_device_status(int clear) {
     if (cudaDeviceSynchronize() != cudaSuccess) return FA_ERR_CUDA;
-    int v = 0;
+    int v = 0, cache = 0;
     if (cudaMemcpyFromSymbol(&v, fa::g_fa_device_status, sizeof(int)) != cudaSuccess)
         return FA_ERR_CUDA;
     if (clear) {
@@ -759,18 +762,20 @@ int fa_device_status(int clear) {
         if (cudaMemcpyToSymbol(fa::g_fa_device_status, &z, sizeof(int)) != cudaSuccess)
             return FA_ERR_CUDA;
     }
-    return v;
+    if (fa_kv4_status_read(clear, &cache) != FA_OK) return FA_ERR_CUDA;
+    return v != 0 ? v : cache;
 }
 
 int fa_last_device_status(fa_stream_t stream) {
     // pageable destination: the copy returns once it has landed, in stream order
-    int v = 0;
+    int v = 0, cache = 0;
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (cudaMemcpyFromSymbolAsync(&v, fa::g_fa_device_status, sizeof(int), 0, cudaMemcpyDeviceToHost,
                                   st) != cudaSuccess)
         return FA_ERR_CUDA;
+    if (fa_kv4_status_read_async(&cache, stream) != FA_OK) return FA_ERR_CUDA;
     if (cudaStreamSynchronize(st) != cudaSuccess) return FA_ERR_CUDA;
-    return v;
+    return v != 0 ? v : cache;
 }
 
 int fa_selftest_timeout(const void* Q, const void* K, const void* V, void* O, int S, int D, int dtype,

@@ -67,6 +67,13 @@
  *                       failed (work-item bounds, the tensor-memory
  *                       allocation, the tile counts of the kernel's roles,
  *                       a stored row's sum); the kernel does not trap
+ *   FA_ERR_BAD_PAGES    reported by fa_device_status() and
+ *                       fa_last_device_status(): a call on the quantised
+ *                       cache met a sequence length or a page number that
+ *                       lies outside the cache (see fa_kv4_cache_t for what
+ *                       was left out)
+ *   FA_ERR_BAD_AXIS     reported likewise: fa_rotary met an axis outside
+ *                       [0, n_axes); that frequency was not turned
  */
 #ifndef FA_GB300_H
 #define FA_GB300_H
@@ -88,7 +95,9 @@ typedef enum {
     FA_ERR_CUDA = 3,
     FA_ERR_TIMEOUT = 4,
     FA_ERR_BAD_SEQLENS = 5,
-    FA_ERR_DEVICE_CHECK = 6
+    FA_ERR_DEVICE_CHECK = 6,
+    FA_ERR_BAD_PAGES = 7,
+    FA_ERR_BAD_AXIS = 8
 } fa_status_t;
 
 typedef enum { FA_F16 = 0, FA_BF16 = 1 } fa_dtype_t;
@@ -293,13 +302,142 @@ int fa_fwd_splitkv_static(const void* Q, const void* K, const void* V, void* O, 
                           int B, int H, int S, int D, int causal, float scale, int dtype,
                           fa_stream_t stream);
 
+/*
+ * Quantised K/V cache.  K and V of earlier tokens are held in pages, in 4 bits
+ * a value and one bf16 scale for 32 values (4.5 bits a value): fa_kv4_write
+ * quantises a call's rows into it, fa_kv4_attention attends over it, and
+ * fa_kv4_read gives plain rows back.  The source pages have no
+ * counterpart; the formulas are stated here.
+ *
+ *   codes   uint8 [pages, 2, H_kv, page_size, D / 2]   (K = 0, V = 1)
+ *   scales  bf16  [pages, 2, H_kv, page_size, D / 32]
+ *
+ * A row (the D values of one token and head) is cut in groups of 32
+ * neighbours.  With x_e the group's element of the largest magnitude (the
+ * first of equals), the scale is s = -x_e / 8 rounded to bf16 and an element x
+ * has the code n = clamp(rint(x / s), -8, 7) + 8 (ties to even), which stands
+ * for s (n - 8).  A group of zeros has s = 0 and codes 8; a group that holds an
+ * infinity or a NaN has s = NaN and codes 8 and stands for NaNs.  The code of
+ * element 32 g + 4 r + j (r < 8, j < 4) is bits 4 j .. 4 j + 3 of the row's
+ * 16-bit word r (D / 32) + g.
+ *
+ * Sequence b has seq_lens[b] tokens in the cache; token i lies at place
+ * i mod page_size of page page_table[b, i / page_size].  A call concerns n_b
+ * rows of it, which are its LAST n_b tokens (seq_lens already counts them):
+ * n_b = cu_seqlens[b+1] - cu_seqlens[b] rows of packed tensors [total, heads, D]
+ * from row cu_seqlens[b], or, when cu_seqlens is NULL, max_seqlen rows of
+ * batched tensors [B, max_seqlen, heads, D].  Rows that come before the first
+ * token (n_b > seq_lens[b], for example the padding in front of a left-padded
+ * prompt) are not written, read back as zeros and attend to nothing (O = 0,
+ * LSE = -inf); so does every row of a sequence of length zero.  Packed rows
+ * outside every sequence are left as they were.
+ *
+ * What lies on the device is checked on the device; nothing outside the cache
+ * is read or written, and the first fault is kept for fa_device_status().
+ *   FA_ERR_BAD_SEQLENS  offsets that fall, leave [0, total], or a sequence of
+ *                       more than max_seqlen rows: the sequence is skipped
+ *   FA_ERR_BAD_PAGES    a length below 0 or above max_pages * page_size: the
+ *                       sequence is skipped.  A page number outside
+ *                       [0, pages) among those of a call's tokens: rows on it
+ *                       are not written, left as they were by a read, and not
+ *                       attended to.
+ * (Skipped: its rows of the cache and of the outputs are left as they were.)
+ * Two sequences may share pages that no call writes; where one call writes a
+ * place twice, that place holds a mix of the rows.
+ *
+ * D is a multiple of 32 up to 256, page_size a multiple of 16; codes and
+ * scales are 16-byte aligned; pages * page_size and the rows of a call are
+ * numbered with an int.  Errors: FA_ERR_INVALID_ARG for NULL pointers, sizes
+ * below 1, or an unknown dtype; FA_ERR_UNSUPPORTED for the limits of this paragraph.
+ */
+typedef struct {
+    void* codes;
+    void* scales;
+    const int* page_table;   /* [B, max_pages], device */
+    const int* seq_lens;     /* [B], device */
+    const int* cu_seqlens;   /* [B + 1], device, or NULL */
+    int B;
+    int max_seqlen;          /* rows of a sequence (cu_seqlens NULL), else the most */
+    int total;               /* rows of the packed tensors; 0 when cu_seqlens is NULL */
+    int pages, max_pages, page_size;
+    int H_kv, D;
+} fa_kv4_cache_t;
+
+/*
+ * Quantises K and V (16-bit, [.., H_kv, D], last axis contiguous) into the
+ * cache.  k_strides / v_strides: strides in elements of (batch, row, head);
+ * the batch's is not used for packed tensors.  They are multiples of 4 and
+ * the base addresses 8-byte aligned, so that slices of a fused projection can
+ * be passed.  K_out, V_out (contiguous, dtype as K; both or neither): what the
+ * cache now stands for, rounded to dtype, for an attention in the same pass
+ * that should see what later ones will; may be K and V themselves when those
+ * are contiguous.
+ */
+int fa_kv4_write(const fa_kv4_cache_t* cache, const void* K, const void* V, const long long* k_strides,
+                 const long long* v_strides, void* K_out, void* V_out, int dtype, fa_stream_t stream);
+
+/* Rows of the cache as contiguous 16-bit K and V [.., H_kv, D] (exact in fp16
+ * where its range allows, rounded once in bf16). */
+int fa_kv4_read(const fa_kv4_cache_t* cache, void* K, void* V, int dtype, fa_stream_t stream);
+
+/*
+ * Attention of the calls' rows over the cache: row i of sequence b is the token at
+ * position p = seq_lens[b] - n_b + i and sees the keys max(0, p - window_left)
+ * .. p (window_left = -1: from 0).  Query head h uses K/V head
+ * h / (H / H_kv).  Q: 16-bit [.., H, D] with strides (batch, row, head) in
+ * elements, multiples of 8; O: contiguous, Q's type; LSE: fp32 [B, H, max_seqlen], or
+ * [H, total] for packed tensors, or NULL.  The keys are split over CTAs
+ * and the parts joined by a second kernel on the same stream, through
+ * `workspace` (16-byte aligned, of fa_kv4_attention_workspace_size bytes for
+ * the same cache, H and dtype on the same device; no initialisation).  Calls
+ * that share a workspace must be ordered on one stream.  A NaN in Q or in a
+ * visible key makes its row NaN, one in a visible value its group's elements.
+ * Errors besides the cache's: FA_ERR_INVALID_ARG for H < 1, H not a multiple
+ * of H_kv, window_left < -1, scale not finite or <= 0, a missing or too small
+ * workspace.
+ */
+int fa_kv4_attention_workspace_size(const fa_kv4_cache_t* cache, int H, int dtype, size_t* bytes);
+int fa_kv4_attention(const fa_kv4_cache_t* cache, const void* Q, const long long* q_strides, void* O, float* LSE,
+                     int H, int window_left, float scale, int dtype, void* workspace, size_t workspace_bytes,
+                     fa_stream_t stream);
+
+/*
+ * Rotary positions with several axes (one for text; time, height and width
+ * for video; ...).  For each token t, head and frequency f < n_freq, the pair
+ * (x_a, x_b) of the head's elements is turned by the angle
+ * positions[t, axes[f]] * inv_freq[f]:
+ *   y_a = x_a cos - x_b sin,   y_b = x_b cos + x_a sin
+ * with (a, b) = (f, f + n_freq), or (2 f, 2 f + 1) when interleaved != 0.
+ * Elements from 2 n_freq on are copied.  inverse != 0 turns the other way,
+ * which is also the gradient: dX = the inverse turn of dY.  Angles are exact to about
+ * 2^-24 of a turn up to positions of 2^24, sums are fp32, the result is rounded once.
+ *   X   [T, H, D] 16-bit with strides (row, head) in elements, last axis
+ *       contiguous; Y the same with strides of its own, and may be X itself
+ *       (same strides) but not overlap it otherwise.
+ *   X2, Y2, H2: a second tensor of the same tokens (the keys); H2 = 0: none.
+ *   positions [T, n_axes] int32, inv_freq [n_freq] double, axes [n_freq]
+ *   int32, contiguous device memory.
+ * 2 n_freq <= D <= 256.  16-byte accesses are used where n_freq, D, the strides
+ * (all multiples of 8) and the base addresses allow it.  Errors:
+ * FA_ERR_INVALID_ARG for NULL pointers, sizes below 1, 2 n_freq > D or an
+ * unknown dtype; FA_ERR_UNSUPPORTED for D > 256, more than 65535 heads or
+ * addresses off their type's alignment.
+ */
+int fa_rotary(const void* X, const long long* x_strides, void* Y, const long long* y_strides, int H,
+              const void* X2, const long long* x2_strides, void* Y2, const long long* y2_strides, int H2,
+              const int* positions, const double* inv_freq, const int* axes, int T, int n_axes, int n_freq, int D,
+              int interleaved, int inverse, int dtype, fa_stream_t stream);
+
 /* Static text for a status code (never NULL). */
 const char* fa_status_string(int status);
 
 /*
  * Device-side status of the calls made so far on the current device:
  * FA_OK, or the first failure seen: FA_ERR_TIMEOUT if some kernel gave up on
- * a wait, FA_ERR_BAD_SEQLENS if fa_fwd_varlen met offsets out of range.  Synchronises
+ * a wait, FA_ERR_BAD_SEQLENS if fa_fwd_varlen (or a call on the quantised
+ * cache) met offsets out of range, FA_ERR_BAD_PAGES if a call on the quantised
+ * cache met a length or page outside it (the attention forward's failures are
+ * reported first).  Synchronises
  * the device.  clear != 0 resets the word to FA_OK.  Returns FA_ERR_CUDA if the
  * status word cannot be read.
  */
@@ -309,7 +447,7 @@ int fa_device_status(int clear);
  * The device status word as the calls enqueued on `stream` so far left it:
  * the word is read after all of that work (a copy ordered on `stream`, then a
  * wait for `stream` alone; other streams keep running).  Returns FA_OK,
- * FA_ERR_TIMEOUT or FA_ERR_BAD_SEQLENS as fa_device_status does, without
+ * FA_ERR_TIMEOUT, FA_ERR_BAD_SEQLENS or FA_ERR_BAD_PAGES as fa_device_status does, without
  * clearing it; FA_ERR_CUDA if the copy or the wait fails.  The word is one per
  * device (the current one) and shared by every stream on it, so a failure of
  * a kernel on another stream that finished before the read shows here too.
