@@ -117,27 +117,31 @@ int decode(const kv4::Cache& c, kv4::Attend a, void* ws, size_t ws_bytes, Decode
     auto* kernel = kv4::decode_kernel<NG, NT, BF16>;
     constexpr int smem = kv4::decode_smem<NG, NT>();
     int sms = 0, ctas = 0;
-    if (!resident(res, kernel, kv4::kWarps * 32, smem, &sms, &ctas)) return FA_ERR_CUDA;
+    if (!resident(res, kernel, kv4::kThreads, smem, &sms, &ctas)) return FA_ERR_CUDA;
     DecodePlan plan;
     const long long items = (static_cast<long long>(c.S) * a.G + R - 1) / R * c.Hkv;
     const long long blocks = (static_cast<long long>(c.max_pages) * c.P + 2 * kv4::kBlock - 1) / kv4::kBlock;
-    if (items * c.B > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
+    // items of a call, and blocks of a sequence, are numbered with an int
+    if (items * c.B > 0x7fffffffLL || items * blocks > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
     plan.items_most = static_cast<int>(items);
-    const long long most = (items * c.B * blocks + kv4::kWarps - 1) / kv4::kWarps;
-    plan.grid = static_cast<int>(std::min<long long>(most, static_cast<long long>(sms) * ctas));
-    const size_t slots = static_cast<size_t>(plan.grid) * 2 * R;
+    const bool whole = blocks <= kv4::kWholeBlocks + 1;
+    const long long most = whole ? items * c.B : (items * c.B * blocks + kv4::kWarps - 1) / kv4::kWarps;
+    plan.grid = static_cast<int>(whole ? most : std::min<long long>(most, static_cast<long long>(sms) * ctas));
+    const size_t slots = whole ? 0 : static_cast<size_t>(plan.grid) * 2 * R;
     plan.bytes = slots * (D * sizeof(float) + sizeof(float2));
     if (only_plan != nullptr) {
         *only_plan = plan;
         return FA_OK;
     }
-    if (ws == nullptr || ws_bytes < plan.bytes) return FA_ERR_INVALID_ARG;
+    if (plan.bytes > 0 && (ws == nullptr || ws_bytes < plan.bytes)) return FA_ERR_INVALID_ARG;
     if (misaligned(ws, 16)) return FA_ERR_UNSUPPORTED;
     a.part_o = static_cast<float*>(ws);
     a.part_ml = reinterpret_cast<float2*>(a.part_o + slots * D);
     a.grid = plan.grid;
-    kernel<<<plan.grid, kv4::kWarps * 32, smem, st>>>(c, a);
+    a.whole = whole ? plan.items_most : 0;
+    kernel<<<plan.grid, kv4::kThreads, smem, st>>>(c, a);
     if (launched() != FA_OK) return FA_ERR_CUDA;
+    if (whole) return FA_OK;
     cudaLaunchAttribute pdl[1];
     pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     pdl[0].val.programmaticStreamSerializationAllowed = 1;

@@ -150,30 +150,60 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
 
 __device__ __forceinline__ float bf16_bits(uint32_t lo16) { return __uint_as_float(lo16 << 16); }
 
-// N 16-bit words at p, in the widest accesses that their alignment (the
-// largest power of two that divides 2 N, at most 16) allows.
+// N 16-bit words, two to a register, read and written in the widest accesses
+// that their alignment (the largest power of two that divides 2 N, at most 16) allows.
 template <int N>
 struct Words {
-    alignas(16) uint16_t w[N];
-    using Unit = std::conditional_t<N % 8 == 0, uint4,
-                 std::conditional_t<N % 4 == 0, uint2, std::conditional_t<N % 2 == 0, uint32_t, uint16_t>>>;
-    static constexpr int kUnits = N * 2 / static_cast<int>(sizeof(Unit));
-    __device__ __forceinline__ void load(const void* p) {
+    static constexpr int kRegs = (N + 1) / 2;
+    uint32_t u[kRegs];
+    using Unit = std::conditional_t<N % 8 == 0, uint4, std::conditional_t<N % 4 == 0, uint2, uint32_t>>;
+
+    __device__ __forceinline__ void clear() {
 #pragma unroll
-        for (int i = 0; i < kUnits; ++i) {
-            const Unit u = static_cast<const Unit*>(p)[i];
-            __builtin_memcpy(w + i * (sizeof(Unit) / 2), &u, sizeof(Unit));
+        for (int i = 0; i < kRegs; ++i) u[i] = 0;
+    }
+    __device__ __forceinline__ void load(const void* p) {
+        if constexpr (N % 2 == 0) {
+#pragma unroll
+            for (int i = 0; i < N * 2 / static_cast<int>(sizeof(Unit)); ++i) {
+                const Unit v = static_cast<const Unit*>(p)[i];
+                __builtin_memcpy(u + i * (sizeof(Unit) / 4), &v, sizeof(Unit));
+            }
+        } else {
+            clear();
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                u[i / 2] |= static_cast<uint32_t>(static_cast<const uint16_t*>(p)[i]) << (16 * (i & 1));
         }
     }
     __device__ __forceinline__ void store(void* p) const {
+        if constexpr (N % 2 == 0) {
 #pragma unroll
-        for (int i = 0; i < kUnits; ++i) {
-            Unit u;
-            __builtin_memcpy(&u, w + i * (sizeof(Unit) / 2), sizeof(Unit));
-            static_cast<Unit*>(p)[i] = u;
+            for (int i = 0; i < N * 2 / static_cast<int>(sizeof(Unit)); ++i) {
+                Unit v;
+                __builtin_memcpy(&v, u + i * (sizeof(Unit) / 4), sizeof(Unit));
+                static_cast<Unit*>(p)[i] = v;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) static_cast<uint16_t*>(p)[i] = static_cast<uint16_t>(get(i));
         }
     }
+    __device__ __forceinline__ uint32_t get(int i) const { return (i & 1) ? u[i / 2] >> 16 : u[i / 2] & 0xffffu; }
+    __device__ __forceinline__ void set(int i, uint32_t w) {   // w < 2^16
+        u[i / 2] = (i & 1) ? (u[i / 2] & 0xffffu) | (w << 16) : (u[i / 2] & 0xffff0000u) | w;
+    }
+    // word i as a bfloat16
+    __device__ __forceinline__ float bf16(int i) const {
+        return __uint_as_float((i & 1) ? u[i / 2] & 0xffff0000u : u[i / 2] << 16);
+    }
 };
+
+// Word i of a below word j of b.
+template <int N, int M>
+__device__ __forceinline__ uint32_t join_words(const Words<N>& a, int i, const Words<M>& b, int j) {
+    return __byte_perm(a.u[i / 2], b.u[j / 2], ((i & 1) ? 0x0032u : 0x0010u) | ((j & 1) ? 0x7600u : 0x5400u));
+}
 
 // ------------------------------------------------------------------- write
 struct RowIo {
@@ -228,6 +258,8 @@ __global__ void __launch_bounds__(kRowThreads) write_kernel(Cache c, RowIo io) {
     }
     constexpr uint32_t kInf = BF16 ? 0x7f80u : 0x7c00u;
     Words<NG> codes, scales;
+    codes.clear();
+    scales.clear();
     uint2 y[NG];
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
@@ -263,8 +295,8 @@ __global__ void __launch_bounds__(kRowThreads) write_kernel(Cache c, RowIo io) {
             word |= ((__float_as_uint(m) + 8u) & 15u) << (4 * j);
             q[j] = __fadd_rn(m, -12582912.f) * s;
         }
-        codes.w[g] = static_cast<uint16_t>(word);
-        scales.w[g] = static_cast<uint16_t>(sb);
+        codes.set(g, word);
+        scales.set(g, sb);
         y[g] = make_uint2(pack16<BF16>(q[0], q[1]), pack16<BF16>(q[2], q[3]));
     }
     if (place == kRowOk) {
@@ -309,21 +341,19 @@ __global__ void __launch_bounds__(kRowThreads) read_kernel(Cache c, RowIo io) {
         codes.load(c.codes + row * (16 * NG) + sub * (2 * NG));
         scales.load(c.scales + row * NG);
     } else {
-#pragma unroll
-        for (int g = 0; g < NG; ++g) {
-            codes.w[g] = 0;
-            scales.w[g] = 0;
-        }
+        codes.clear();
+        scales.clear();
     }
     uint16_t* dst = static_cast<uint16_t*>(which == 0 ? io.k_out : io.v_out) +
                     (static_cast<long long>(t) * c.Hkv + head) * D;
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
-        const float s = bf16_bits(scales.w[g]);
+        const float s = scales.bf16(g);
+        const uint32_t word = codes.get(g);
         float q[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const int n = static_cast<int>((codes.w[g] >> (4 * j)) & 15u) - 8;
+            const int n = static_cast<int>((word >> (4 * j)) & 15u) - 8;
             q[j] = place == kRowOk ? static_cast<float>(n) * s : 0.f;
         }
         *reinterpret_cast<uint2*>(dst + g * kGroup + sub * 4) =

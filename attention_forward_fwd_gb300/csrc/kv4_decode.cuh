@@ -13,16 +13,17 @@
 // clock, so the unpacking is what has to be cheap:
 //  * Keys are the M side of both products: one m16n8k16 eats 256 codes for 8
 //    query rows (with the queries on the M side it would eat 128).
-//  * K's codes go to the tensor cores as fp16 subnormals: the nibble n in the
-//    low bits of a half IS n 2^-24, in bits 4..7 it is n 2^-20, so a pair of
-//    codes costs one AND.  Q's elements for the second kind carry a factor
-//    1/16, and the accumulator of a group starts at -8 sum(q) 2^-24, which
-//    turns n into n - 8.  Each group's product is scaled by the key's fp32
-//    scale as it is added up, so nothing of K is rounded.
-//  * V's codes are paired over two keys (one byte permutation), then
-//    (x & mask | 0x6400) - 1032 gives n - 8 in fp16 exactly.  The offset is
-//    taken off here and not at the end, because the accumulator runs over the
-//    whole context and would carry an offset many times the result.
+//  * K's codes go to the tensor cores as fp16 subnormals: in bits 4..7 of a half
+//    the nibble n IS n 2^-20, so a pair of codes costs an AND and a shift. The
+//    accumulator of a group starts at -8 sum(q) 2^-20, which turns n into n - 8,
+//    and each group's product is scaled by the key's fp32 scale as it is added up.
+//    (Bits 0..3 would need fewer shifts, but the tensor cores align a subnormal by
+//    its exponent field, and n 2^-24 has 10 bits of nothing in front: results were
+//    off by 2^-14 of a code.)
+//  * V's codes are paired over two keys (one byte permutation); (x & mask | 0x6400)
+//    minus 1032 or 1152 is n - 8 or 16 (n - 8) in fp16, a normal number.  The
+//    offset comes off here, because the accumulator runs over the whole context
+//    and would carry an offset many times the result.
 //  * The scale of V belongs to (key, group): it multiplies P, one fp16 matrix
 //    operand for each group, turned from the accumulator's layout to the
 //    operand's by movmatrix.
@@ -34,9 +35,16 @@
 // row and cut into equal ranges, one for each CTA (the lengths are on the
 // device only, so the cut is made there).  An item that a cut goes through
 // leaves partial results, which combine_kernel joins in the order of the keys.
-// Within a CTA the four warps take the blocks in turn, each with a ring of
-// its own of asynchronous bulk copies (no barrier of the CTA in the loop; the
-// copies run ahead over the ends of items), and join at the end of an item.
+// Within a CTA four warps cut the range again and work alone, each with a ring
+// of its own that its lanes fill with 16-byte asynchronous copies (they run ahead
+// over the ends of items; no barrier but the warp's).  Bulk copies by a fifth
+// warp took more instructions: their operands are uniform, so that the lanes' copies
+// went out one by one.  Items that lie inside a warp's range are written by it; the parts of the others
+// (at most two a warp) are joined once, at the end of the CTA.  Sharing each
+// item's blocks out to the warps in turn, with a join for each item, left
+// the warps waiting for one another: batch of 64 ragged contexts, 84 us.
+// Short contexts (all of an item's blocks: kWholeBlocks) are not cut between
+// CTAs: a CTA an item, one launch.
 #pragma once
 
 #include "kv4_cache.cuh"
@@ -44,11 +52,14 @@
 namespace kv4 {
 
 constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
 constexpr int kStages = 2;
 constexpr int kBlock = 32;              // keys a block
 constexpr float kLazy = 8.f;            // p may reach 2^kLazy before m moves
 constexpr int kHead = 7;                // p s 2^(kHead - E) < 2^(kLazy + kHead) < 65504
+constexpr int kWholeBlocks = 16;        // most blocks of an item that is never cut
 constexpr float kNegInf = -INFINITY;
+constexpr uint32_t kMid = 0x00f000f0u;  // bits 4..7 of both halves
 
 struct Attend {
     const void* q;
@@ -62,6 +73,7 @@ struct Attend {
     float* part_o;                       // [2 grid][8 NT][D]
     float2* part_ml;                     // [2 grid][8 NT]: reference and sum
     int grid;                            // CTAs of decode_kernel
+    int whole;                           // nonzero: a CTA an item, of this many items a sequence
 };
 
 template <int NG>
@@ -70,11 +82,20 @@ struct Tile {
     static constexpr int kCodes = kBlock * 16 * NG;        // bytes of K's (V's) codes in a block
     static constexpr int kScales = kBlock * 2 * NG;
     static constexpr int kStage = 2 * (kCodes + kScales);
+    static constexpr int kRing = kWarps * kStages * kStage;
 };
 
+// A warp's part of an item that it does not hold whole: [8 NT][D + 4] sums
+// (the last 4 only pad the rows off one another's banks).
+template <int NG, int NT>
+constexpr int kPartFloats = 8 * NT * (Tile<NG>::D + 4);
+
+// The ring, a part for each warp (the second one, of its last item, goes into
+// its own ring, which is empty by then), the rest.
 template <int NG, int NT>
 constexpr int decode_smem() {
-    return kWarps * kStages * Tile<NG>::kStage + kWarps * 8 * NT * (Tile<NG>::D + 4) * 4 + 1024;
+    static_assert(kPartFloats<NG, NT> * 4 <= kStages * Tile<NG>::kStage, "a part fits the ring");
+    return Tile<NG>::kRing + kWarps * kPartFloats<NG, NT> * 4 + 2048;
 }
 
 // The rows of the call for a sequence as items: tiles x heads, each of `blocks` key blocks from key `first`.
@@ -97,44 +118,70 @@ __device__ __forceinline__ Work work_of(const Cache& c, const Attend& a, int b, 
     return w;
 }
 
-// All blocks of all sequences before b (b = B: of the call), by the whole CTA.
-__device__ __forceinline__ long long scan_blocks(const Cache& c, const Attend& a, int tile_rows, bool tell,
-                                                 long long target, int* found, long long* found_at,
-                                                 long long* sh) {
-    // Each round takes blockDim.x sequences; *found is the last b whose blocks
-    // start at or before `target` and do not end there.
-    long long base = 0;
+// The blocks of a call in a row: their number, and the sequence that holds
+// block quota * blockIdx.x with the number of its first block.  By the whole
+// CTA; each round takes blockDim.x sequences, and a second pass is made only
+// when there are more than that.
+struct Range {
+    long long all, quota, at;
+    int b;
+};
+
+__device__ __forceinline__ long long quota_of(long long all, int grid) {
+    return max((all + grid - 1) / grid, static_cast<long long>(kWarps));
+}
+
+__device__ __forceinline__ Range find_range(const Cache& c, const Attend& a, int tile_rows, long long* sh) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
-    for (int b0 = 0; b0 < c.B; b0 += blockDim.x) {
-        const int b = b0 + threadIdx.x;
-        long long mine = 0;
-        if (b < c.B) {
-            const Work w = work_of(c, a, b, tile_rows, tell);
-            mine = static_cast<long long>(w.items) * w.blocks;
-        }
-        long long x = mine;
+    Range r;
+    r.all = 0;
+    r.quota = 0;
+    for (int pass = 0; pass < 2; ++pass) {
+        long long base = 0;
+        for (int b0 = 0; b0 < c.B; b0 += blockDim.x) {
+            const int b = b0 + threadIdx.x;
+            long long mine = 0;
+            if (b < c.B) {
+                const Work w = work_of(c, a, b, tile_rows, pass == 0 && blockIdx.x == 0);
+                mine = static_cast<long long>(w.items) * w.blocks;
+            }
+            long long x = mine;
 #pragma unroll
-        for (int m = 1; m < 32; m <<= 1) {
-            const long long y = __shfl_up_sync(0xffffffffu, x, m);
-            if (lane >= m) x += y;
+            for (int m = 1; m < 32; m <<= 1) {
+                const long long y = __shfl_up_sync(0xffffffffu, x, m);
+                if (lane >= m) x += y;
+            }
+            __syncthreads();
+            if (lane == 31) sh[warp] = x;
+            __syncthreads();
+            long long before = base, here = 0;
+            for (int i = 0; i < nw; ++i) {
+                if (i < warp) before += sh[i];
+                here += sh[i];
+            }
+            const long long start = before + x - mine;
+            base += here;
+            const bool one = c.B <= static_cast<int>(blockDim.x);
+            if (one) {
+                r.all = base;
+                r.quota = quota_of(base, a.grid);
+            }
+            if (one || pass == 1) {
+                const long long lo = r.quota * blockIdx.x;
+                if (mine > 0 && start <= lo && lo < start + mine) {
+                    sh[14] = b;
+                    sh[15] = start;
+                }
+            }
         }
-        __syncthreads();
-        if (lane == 31) sh[warp] = x;
-        __syncthreads();
-        long long before = base, all = 0;
-        for (int i = 0; i < nw; ++i) {
-            if (i < warp) before += sh[i];
-            all += sh[i];
-        }
-        const long long start = before + x - mine;
-        if (mine > 0 && start <= target && target < start + mine) {
-            *found = b;
-            *found_at = start;
-        }
-        base += all;
+        if (c.B <= static_cast<int>(blockDim.x)) break;
+        r.all = base;
+        r.quota = quota_of(base, a.grid);
     }
     __syncthreads();
-    return base;
+    r.b = static_cast<int>(sh[14]);
+    r.at = sh[15];
+    return r;
 }
 
 // A warp's place in the row of blocks.
@@ -160,23 +207,13 @@ struct Cursor {
     }
 };
 
-__device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity) {
-    if (fa::ptx::mbar_try_wait(bar, parity)) return true;
-    const uint64_t t0 = fa::ptx::globaltimer();
-    for (uint32_t n = 1;; ++n) {
-        if (fa::ptx::mbar_try_wait(bar, parity)) return true;
-        if ((n & 31u) == 0 && fa::ptx::globaltimer() - t0 > 1000000000ull) {
-            report(kStatusTimeout);
-            return false;
-        }
-    }
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
-
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-        "l"(src), "r"(bytes), "r"(bar)
-        : "memory");
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {   // all but the last N groups of this thread have landed
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 __device__ __forceinline__ void mma16816(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
@@ -198,114 +235,187 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
 // both products.
 __device__ __forceinline__ int key_of(int r) { return r ^ ((r >> 1) & 1); }
 
-// A lane's codes of a row of K: 2 r's, all groups, as pairs (r = 2 c, 2 c + 1).
+// n - 8 of the codes in bits 0..3, and 16 (n - 8) of those in bits 4..7, of
+// each half of u, in fp16: 1024 + x is 0x6400 | x.
+__device__ __forceinline__ uint32_t half_sub(uint32_t y, uint32_t c) {
+    const __half2 z = __hsub2(*reinterpret_cast<const __half2*>(&y), *reinterpret_cast<const __half2*>(&c));
+    return *reinterpret_cast<const uint32_t*>(&z);
+}
+__device__ __forceinline__ uint32_t low_codes(uint32_t u) {
+    return half_sub((u & 0x000f000fu) | 0x64006400u, 0x64086408u);
+}
+__device__ __forceinline__ uint32_t high_codes(uint32_t u) {
+    return half_sub((u & kMid) | 0x64006400u, 0x64806480u);
+}
+
+// Where warp `warp` starts among its CTA's blocks.
+__device__ __forceinline__ int share(int blocks, int warp) {
+    return static_cast<int>(static_cast<long long>(blocks) * warp / kWarps);
+}
+
+// A warp's copies: the blocks of its range one after the other, each in runs of
+// 32 or 16 keys that lie together in a page.  A whole run is copied as soon
+// as one of its keys belongs to the sequence.
 template <int NG>
-__device__ __forceinline__ uint32_t k_pair(const Words<2 * NG>& w, int g) {
-    // halfwords g and NG + g; PRMT where they sit in registers
-    return static_cast<uint32_t>(w.w[g]) | (static_cast<uint32_t>(w.w[NG + g]) << 16);
+struct Copier {
+    Cursor cur;
+    int left;              // blocks not copied yet
+    int head, item;
+    int page[2];           // of the block at `cur`; -1: nothing to copy
+
+    // Asks for the pages of the block at `cur`, a block ahead of their use.
+    __device__ __forceinline__ void look_up(const Cache& c, int run_shift) {
+        page[0] = page[1] = -1;
+        if (left <= 0) return;
+        const int key0 = cur.w.first + cur.blk * kBlock;
+        const int* row = c.table + static_cast<long long>(cur.b) * c.max_pages;
+        if (key0 < cur.w.len) page[0] = __ldg(row + key0 / c.P);
+        if (run_shift == 4 && key0 + 16 < cur.w.len) page[1] = __ldg(row + (key0 + 16) / c.P);
+    }
+
+    // Copies the block at `cur` to `st` and moves on; bit i of the result: the
+    // i-th 16 keys are there.
+    __device__ __forceinline__ uint32_t copy(const Cache& c, const Attend& a, int tile_rows, int run_shift, uint8_t* st) {
+        uint32_t in = 0;
+        if (left > 0) {
+            const int lane = threadIdx.x & 31;
+            if (item != cur.item) {
+                item = cur.item;
+                head = item / cur.w.tiles;
+            }
+            const int key0 = cur.w.first + cur.blk * kBlock;
+            const uint8_t* codes[2];
+            const uint16_t* scales[2];
+            const long long v_off = static_cast<long long>(c.Hkv) * c.P;   // rows from K to V
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const bool same = i == 1 && run_shift == 5;
+                const int pg = same ? page[0] : page[i];
+                const bool asked = key0 + 16 * (same ? 0 : i) < cur.w.len;
+                const bool ok = asked && pg >= 0 && pg < c.pages;
+                if (asked && !ok) report(kStatusBadPages);
+                if (ok) in |= 1u << i;
+                const long long row = (static_cast<long long>(ok ? pg : 0) * 2 * c.Hkv + head) * c.P + (key0 + 16 * i) % c.P;
+                codes[i] = c.codes + row * (16 * NG);
+                scales[i] = c.scales + row * NG;
+            }
+            const uint32_t dst = fa::ptx::smem_addr(st);
+            // codes: NG chunks of 16 bytes a key, 32 NG a block
+#pragma unroll
+            for (int i = 0; i < NG; ++i) {
+                const int q = i * 32 + lane;
+                const bool second = q >= 16 * NG;
+                if ((in >> (second ? 1 : 0)) & 1u) {
+                    const uint8_t* src = codes[second ? 1 : 0] + (second ? q - 16 * NG : q) * 16;
+                    copy16(dst + q * 16, src);
+                    copy16(dst + Tile<NG>::kCodes + q * 16, src + v_off * (16 * NG));
+                }
+            }
+            // scales: 4 NG chunks a block, K's before V's
+#pragma unroll
+            for (int i = 0; i < (8 * NG + 31) / 32; ++i) {
+                const int q = i * 32 + lane, which = q >= 4 * NG ? 1 : 0, qq = q - which * 4 * NG;
+                const bool second = qq >= 2 * NG;
+                if (q < 8 * NG && ((in >> (second ? 1 : 0)) & 1u)) {
+                    const uint16_t* src = scales[second ? 1 : 0] + (second ? qq - 2 * NG : qq) * 8 + which * v_off * NG;
+                    copy16(dst + 2 * Tile<NG>::kCodes + q * 16, src);
+                }
+            }
+            --left;
+            ++cur.blk;
+            if (left > 0) cur.settle(c, a, tile_rows);
+        }
+        copies_commit();
+        look_up(c, run_shift);
+        return in;
+    }
+};
+
+// What the warps of a CTA left to be joined, in the order of the blocks: part 0
+// carries an item on, part 1 starts one and does not end it.
+struct Part {
+    int b, item;      // b = -1: none
+    int ends;         // the item ends with it
+};
+
+// O and LSE of one row's four elements from sums in units of 2^m.
+template <bool BF16>
+__device__ __forceinline__ void write_row(const Cache& c, const Attend& a, const Work& w, int b, int D, int rho, int head,
+                                          int d, float4 o, float m, float l, bool lse) {
+    const int qi = rho / a.G, h = head * a.G + (rho - qi * a.G);
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    uint16_t* dst = static_cast<uint16_t*>(a.o) + (static_cast<long long>(w.row0 + qi) * a.H + h) * D + d;
+    *reinterpret_cast<uint2*>(dst) =
+        make_uint2(pack16<BF16>(o.x * inv, o.y * inv), pack16<BF16>(o.z * inv, o.w * inv));
+    if (lse)
+        a.lse[(c.cu != nullptr ? w.row0 : b * a.lse_batch) + h * a.lse_head + qi] =
+            l == 0.f ? kNegInf : (m + log2f(l)) * 0.6931471805599453f;
 }
 
 template <int NG, int NT, bool BF16>
-__global__ void __launch_bounds__(kWarps * 32) decode_kernel(Cache c, Attend a) {
-    constexpr int D = NG * kGroup, R = 8 * NT;
+__global__ void __launch_bounds__(kThreads, NG <= 4 && NT == 1 ? 3 : 2) decode_kernel(Cache c, Attend a) {
+    constexpr int D = NG * kGroup, R = 8 * NT, kStage = Tile<NG>::kStage;
+    constexpr int kPart = kPartFloats<NG, NT>;
     extern __shared__ __align__(128) uint8_t smem[];
     uint8_t* ring = smem;
-    float* join = reinterpret_cast<float*>(smem + kWarps * kStages * Tile<NG>::kStage);   // [warp][R][D + 4]
-    uint8_t* tail = reinterpret_cast<uint8_t*>(join + kWarps * R * (D + 4));
-    float2* join_ml = reinterpret_cast<float2*>(tail);                                    // [warp][R], 512 bytes
-    uint64_t* bars = reinterpret_cast<uint64_t*>(tail + 512);                             // [warp][stage], 64
-    uint32_t* runs = reinterpret_cast<uint32_t*>(tail + 576);                             // [warp][stage]
-    long long* scan = reinterpret_cast<long long*>(tail + 640);                           // [warps]
-    int* sh_b = reinterpret_cast<int*>(tail + 704);
-    long long* sh_at = reinterpret_cast<long long*>(tail + 712);
+    float* join = reinterpret_cast<float*>(smem + Tile<NG>::kRing);                       // [warp] part 0
+    uint8_t* tail = reinterpret_cast<uint8_t*>(join + kWarps * kPart);
+    float2* join_ml = reinterpret_cast<float2*>(tail);                                    // [warp][part][R], 1024 bytes
+    long long* scan = reinterpret_cast<long long*>(tail + 1024);                          // 16
+    Part* parts = reinterpret_cast<Part*>(tail + 1152);                                   // [warp][part]
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = lane >> 2, cc = lane & 3;
-    if (tid < kWarps * kStages) {
-        fa::ptx::mbar_init(fa::ptx::smem_addr(bars + tid), 1);
-        fa::ptx::fence_barrier_init();
+
+    // ---- this CTA's blocks: `blocks` from block seg.blk of item seg.item of sequence seg.b on
+    Cursor seg;
+    int blocks;
+    if (a.whole) {
+        seg.b = blockIdx.x / a.whole;
+        seg.item = blockIdx.x - seg.b * a.whole;
+        seg.blk = 0;
+        seg.w = work_of(c, a, seg.b, R, tid == 0 && seg.item == 0);
+        if (seg.item >= seg.w.items) return;
+        blocks = seg.w.blocks;
+    } else {
+        const Range range = find_range(c, a, R, scan);
+        fa::ptx::launch_dependents();
+        const long long lo = range.quota * blockIdx.x;
+        if (lo >= range.all) return;
+        blocks = static_cast<int>(min(range.all - lo, range.quota));
+        seg.b = range.b;
+        seg.w = work_of(c, a, seg.b, R, false);
+        const int off = static_cast<int>(lo - range.at);   // blocks of one sequence are numbered with an int
+        seg.item = off / seg.w.blocks;
+        seg.blk = off - seg.item * seg.w.blocks;
     }
-
-    // ---- this CTA's range of blocks
-    const long long all = scan_blocks(c, a, R, blockIdx.x == 0, -1, sh_b, sh_at, scan);
-    const long long quota = max((all + a.grid - 1) / a.grid, static_cast<long long>(kWarps));
-    const long long lo = quota * blockIdx.x, hi = min(all, lo + quota);
-    fa::ptx::launch_dependents();
-    if (lo >= hi) return;
-    scan_blocks(c, a, R, false, lo, sh_b, sh_at, scan);
-
-    Cursor prod;   // the copies' place
-    prod.b = *sh_b;
-    prod.w = work_of(c, a, prod.b, R, false);
-    const long long off = lo - *sh_at;
-    prod.item = static_cast<int>(off / prod.w.blocks);
-    prod.blk = static_cast<int>(off % prod.w.blocks);
-    Cursor seg = prod;   // the CTA's place, the same in every warp
-    prod.blk += warp;
-    prod.settle(c, a, R);
-    long long prod_x = lo + warp;
-
-    uint8_t* my_ring = ring + warp * kStages * Tile<NG>::kStage;
-    bool dead = false;
-    const int run = (c.P % kBlock) == 0 ? kBlock : 16;   // tokens that lie together
-    auto issue = [&](int stage) {
-        if (prod_x >= hi) return;
-        const uint32_t bar = fa::ptx::smem_addr(bars + warp * kStages + stage);
-        const int head = prod.item / prod.w.tiles;
-        const int key0 = prod.w.first + prod.blk * kBlock;
-        const int left = prod.w.len - key0;              // may be <= 0: a sequence without keys
-        // lane: (run of the block, K or V, codes or scales)
-        const int sub = lane >> 2, which = (lane >> 1) & 1, scales = lane & 1;
-        const int tok = key0 + sub * run;
-        const int want = min(run, (left - sub * run + 15) & ~15);
-        bool ok = sub * run < kBlock && want > 0;
-        int page = 0;
-        if (ok) {
-            page = __ldg(c.table + static_cast<long long>(prod.b) * c.max_pages + tok / c.P);
-            if (page < 0 || page >= c.pages) {
-                report(kStatusBadPages);
-                ok = false;
-            }
-        }
-        const long long row = ((static_cast<long long>(page) * 2 + which) * c.Hkv + head) * c.P + tok % c.P;
-        const uint32_t bytes = ok ? static_cast<uint32_t>(want) * (scales ? 2 * NG : 16 * NG) : 0;
-        uint32_t sum = bytes;
+    uint8_t* my_ring = ring + warp * kStages * kStage;
+    int x = share(blocks, warp);                            // this warp's next block
+    const int x_end = share(blocks, warp + 1);
+    if (lane < 2) parts[warp * 2 + lane].b = -1;
+    __syncwarp();
+    seg.blk += x;
+    if (x < x_end) seg.settle(c, a, R);
+    const int run_shift = (c.P % kBlock) == 0 ? 5 : 4;
+    Copier<NG> copier;
+    copier.cur = seg;
+    copier.left = x_end - x;
+    copier.head = 0;
+    copier.item = -1;
+    copier.look_up(c, run_shift);
+    uint32_t there[kStages];
 #pragma unroll
-        for (int m = 16; m; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
-        const uint32_t mask = __ballot_sync(0xffffffffu, ok);
-        if (lane == 0) {
-            runs[warp * kStages + stage] = (mask & 1u) | ((mask >> 4) & 1u) << 1;
-            fa::ptx::mbar_arrive_expect_tx(bar, sum);
-        }
-        __syncwarp();
-        if (ok) {
-            uint8_t* base = my_ring + stage * Tile<NG>::kStage;
-            uint8_t* dst = scales ? base + 2 * Tile<NG>::kCodes + which * Tile<NG>::kScales + sub * run * 2 * NG
-                                  : base + which * Tile<NG>::kCodes + sub * run * 16 * NG;
-            const void* src = scales ? static_cast<const void*>(c.scales + row * NG)
-                                     : static_cast<const void*>(c.codes + row * (16 * NG));
-            bulk_load(fa::ptx::smem_addr(dst), src, bytes, bar);
-        }
-        prod_x += kWarps;
-        prod.blk += kWarps;
-        if (prod_x < hi) prod.settle(c, a, R);
-    };
-#pragma unroll
-    for (int s = 0; s < kStages; ++s) issue(s);
-
-    long long x = lo + warp;    // this warp's next block
+    for (int i = 0; i < kStages; ++i) there[i] = copier.copy(c, a, R, run_shift, my_ring + i * kStage);
     int stage = 0;
-    uint32_t parity = 0;
     const uint16_t* q16 = static_cast<const uint16_t*>(a.q);
 
-    for (long long seg_lo = lo; seg_lo < hi;) {
-        // ---- one item, or the part of it that is this CTA's
+    while (x < x_end) {
+        // ---- one item, or the part of it that is this warp's
         const Work w = seg.w;
-        const long long seg_hi = min(hi, seg_lo + (w.blocks - seg.blk));
+        const int seg_blocks = min(x_end - x, w.blocks - seg.blk);
         const int head = seg.item / w.tiles, tile = seg.item - head * w.tiles;
         const int rows = min(R, w.n * a.G - tile * R);
 
-        // ---- Q: fp16 with each row's largest magnitude in [2^11, 2^12), the
-        // elements that meet codes in bits 4..7 divided by 16
+        // ---- Q: fp16 with each row's largest magnitude in [2^11, 2^12)
         uint32_t qf[NT][NG][4];
         float cinit[NT][NG][2], fac[NT][2];
         int hi_key[NT][2], lo_key[NT][2];
@@ -338,48 +448,54 @@ __global__ void __launch_bounds__(kWarps * 32) decode_kernel(Cache c, Attend a) 
             // 2^up brings `most` to [2^11, 2^12)
             int up = most > 0.f ? 138 - static_cast<int>((__float_as_uint(most) >> 23) & 255u) : 0;
             up = max(-90, min(100, up));
-            const float mul = __uint_as_float(static_cast<uint32_t>(127 + up) << 23), mul16 = mul * 0.0625f;
+            const float mul = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
             float qsum[NG];
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
-                // elements 8 cc + e: e = j and 4 + j pair up; j odd sits in bits 4..7
+                // elements 8 cc + e: e = j and 4 + j pair up
                 const float2 e01 = to_f32x2<BF16>(raw[g].x), e23 = to_f32x2<BF16>(raw[g].y);
                 const float2 e45 = to_f32x2<BF16>(raw[g].z), e67 = to_f32x2<BF16>(raw[g].w);
                 qf[t][g][0] = pack16<false>(e01.x * mul, e45.x * mul);       // j = 0
                 qf[t][g][1] = pack16<false>(e23.x * mul, e67.x * mul);       // j = 2
-                qf[t][g][2] = pack16<false>(e01.y * mul16, e45.y * mul16);   // j = 1
-                qf[t][g][3] = pack16<false>(e23.y * mul16, e67.y * mul16);   // j = 3
+                qf[t][g][2] = pack16<false>(e01.y * mul, e45.y * mul);       // j = 1
+                qf[t][g][3] = pack16<false>(e23.y * mul, e67.y * mul);       // j = 3
                 const float2 s0 = to_f32x2<false>(qf[t][g][0]), s1 = to_f32x2<false>(qf[t][g][1]);
                 const float2 s2 = to_f32x2<false>(qf[t][g][2]), s3 = to_f32x2<false>(qf[t][g][3]);
-                qsum[g] = ((s0.x + s0.y) + (s1.x + s1.y)) + 16.f * ((s2.x + s2.y) + (s3.x + s3.y));
+                qsum[g] = ((s0.x + s0.y) + (s1.x + s1.y)) + ((s2.x + s2.y) + (s3.x + s3.y));
                 qsum[g] += __shfl_xor_sync(0xffffffffu, qsum[g], 1);
                 qsum[g] += __shfl_xor_sync(0xffffffffu, qsum[g], 2);
-                qsum[g] *= -8.f * 5.9604644775390625e-8f;                    // -8 2^-24
+                qsum[g] *= -8.f * 9.5367431640625e-7f;                       // -8 2^-20
             }
-            // z = S 2^24 2^-up scale log2 e
-            const float f = a.scale * 1.4426950408889634f * 16777216.f *
-                            __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
+            // z = S 2^20 2^-up scale log2 e
+            const float f = fmaxf(a.scale * 1.4426950408889634f * 1048576.f *
+                                      __uint_as_float(static_cast<uint32_t>(127 - up) << 23), 1.17549435e-38f);
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int from = (2 * cc + e) * 4;   // a lane that holds row 2 cc + e
                 fac[t][e] = __shfl_sync(0xffffffffu, f, from);
 #pragma unroll
                 for (int g = 0; g < NG; ++g) cinit[t][g][e] = __shfl_sync(0xffffffffu, qsum[g], from);
+                // rows past the tile's last one see everything; nobody reads what comes of them
                 const int rr = t * 8 + 2 * cc + e;
-                const int pos = rr < rows ? w.len - w.n + (tile * R + rr) / a.G : -1;
-                hi_key[t][e] = pos;
-                lo_key[t][e] = a.window >= 0 ? max(0, pos - a.window) : 0;
+                const int pos = w.len - w.n + (tile * R + rr) / a.G;
+                hi_key[t][e] = rr < rows ? pos : 0x7fffffff;
+                lo_key[t][e] = rr < rows && a.window >= 0 ? max(0, pos - a.window) : 0;
             }
         }
+        // keys that every row of the tile sees
+        const int all_hi = w.len - w.n + tile * R / a.G;
+        const int all_lo = a.window >= 0 ? max(0, w.len - w.n + (tile * R + rows - 1) / a.G - a.window) : 0;
 
         float acc[NT][NG][2][4];
-        float m_ref[NT][2], l_sum[NT][2];
+        float thr[NT][2], neg_ref[NT][2], l_sum[NT][2];   // raw score that moves the reference; -(m - kHead + E)
+        float m_ref[NT][2];
         int e_ref = -90;
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                m_ref[t][e] = kNegInf;
+                m_ref[t][e] = thr[t][e] = kNegInf;
+                neg_ref[t][e] = static_cast<float>(kHead + 90);
                 l_sum[t][e] = 0.f;
             }
 #pragma unroll
@@ -388,13 +504,13 @@ __global__ void __launch_bounds__(kWarps * 32) decode_kernel(Cache c, Attend a) 
                 for (int i = 0; i < 8; ++i) acc[t][g][i >> 2][i & 3] = 0.f;
         }
 
-        for (; x < seg_hi; x += kWarps) {
-            const int key0 = w.first + (seg.blk + static_cast<int>(x - seg_lo)) * kBlock;
-            if (!dead && !wait_bounded(fa::ptx::smem_addr(bars + warp * kStages + stage), parity)) dead = true;
-            const uint8_t* st = my_ring + stage * Tile<NG>::kStage;
-            const uint32_t good = runs[warp * kStages + stage];
-            // bit r16 of `in`: sub-tile r16 (16 keys) has been copied
-            const uint32_t in = run == kBlock ? ((good & 1u) ? 3u : 0u) : good;
+        for (int blk = 0; blk < seg_blocks; ++blk) {
+            const int key0 = w.first + (seg.blk + blk) * kBlock;
+            copies_wait<kStages - 1>();
+            __syncwarp();
+            uint8_t* st = my_ring + stage * kStage;
+            const uint32_t in = there[0];
+            const bool edge = key0 + (kBlock - 1) > all_hi || key0 < all_lo || in != 3u;
 
             // ---- S^T = K Q^T for 2 x 16 keys
             float s[2][NT][4];
@@ -408,70 +524,71 @@ __global__ void __launch_bounds__(kWarps * 32) decode_kernel(Cache c, Attend a) 
                 s0.load(st + 2 * Tile<NG>::kCodes + k0 * 2 * NG);
                 s1.load(st + 2 * Tile<NG>::kCodes + k1 * 2 * NG);
 #pragma unroll
-                for (int t = 0; t < NT; ++t)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) s[kt][t][i] = 0.f;
-#pragma unroll
                 for (int g = 0; g < NG; ++g) {
-                    const uint32_t x0 = k_pair<NG>(c0, g), x1 = k_pair<NG>(c1, g);
-                    const uint32_t a_even[4] = {x0 & 0x000f000fu, x1 & 0x000f000fu, (x0 >> 8) & 0x000f000fu,
-                                                (x1 >> 8) & 0x000f000fu};
-                    const uint32_t a_odd[4] = {x0 & 0x00f000f0u, x1 & 0x00f000f0u, (x0 >> 8) & 0x00f000f0u,
-                                               (x1 >> 8) & 0x00f000f0u};
-                    const float f0 = bf16_bits(s0.w[g]), f1 = bf16_bits(s1.w[g]);
+                    // r = 2 cc below r = 2 cc + 1
+                    const uint32_t x0 = join_words(c0, g, c0, NG + g), x1 = join_words(c1, g, c1, NG + g);
+                    const uint32_t y0 = x0 >> 8, y1 = x1 >> 8;
+                    // shifts to the left as products: the FMA pipe has room, the ALU has not
+                    const uint32_t a_even[4] = {(x0 * 16u) & kMid, (x1 * 16u) & kMid, (y0 * 16u) & kMid, (y1 * 16u) & kMid};
+                    const uint32_t a_odd[4] = {x0 & kMid, x1 & kMid, y0 & kMid, y1 & kMid};
+                    const float f0 = s0.bf16(g), f1 = s1.bf16(g);
 #pragma unroll
                     for (int t = 0; t < NT; ++t) {
                         float d[4] = {cinit[t][g][0], cinit[t][g][1], cinit[t][g][0], cinit[t][g][1]};
                         mma16816(d, a_even, qf[t][g][0], qf[t][g][1]);
                         mma16816(d, a_odd, qf[t][g][2], qf[t][g][3]);
-                        s[kt][t][0] = fmaf(f0, d[0], s[kt][t][0]);
-                        s[kt][t][1] = fmaf(f0, d[1], s[kt][t][1]);
-                        s[kt][t][2] = fmaf(f1, d[2], s[kt][t][2]);
-                        s[kt][t][3] = fmaf(f1, d[3], s[kt][t][3]);
+                        s[kt][t][0] = g == 0 ? f0 * d[0] : fmaf(f0, d[0], s[kt][t][0]);
+                        s[kt][t][1] = g == 0 ? f0 * d[1] : fmaf(f0, d[1], s[kt][t][1]);
+                        s[kt][t][2] = g == 0 ? f1 * d[2] : fmaf(f1, d[2], s[kt][t][2]);
+                        s[kt][t][3] = g == 0 ? f1 * d[3] : fmaf(f1, d[3], s[kt][t][3]);
                     }
                 }
             }
+            // V's scales
+            Words<NG> sv[2][2];
+#pragma unroll
+            for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    sv[kt][h].load(st + 2 * Tile<NG>::kCodes + Tile<NG>::kScales + (kt * 16 + h * 8 + key_of(r)) * 2 * NG);
 
-            // ---- z, masks, and whether a reference has to move
-            bool grow = false;
+            if (edge) {
+                // Masked scores are -inf.  V's scales are zero where the key was
+                // not copied or lies past the sequence (there may be anything
+                // there, NaN included).
+#pragma unroll
+                for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int key = key0 + kt * 16 + h * 8 + key_of(r);
+                        const bool have = (in >> kt) & 1u;
+                        if (!(have && key < w.len)) sv[kt][h].clear();
+#pragma unroll
+                        for (int t = 0; t < NT; ++t)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e)
+                                if (!(have && key <= min(hi_key[t][e], w.len - 1) && key >= lo_key[t][e]))
+                                    s[kt][t][h * 2 + e] = kNegInf;
+                    }
+            }
+
+            // ---- whether a reference has to move: a score past thr, or a
+            // scale of 2^E or more (or a NaN, whose bits are larger still)
+            uint32_t big = 0;
+#pragma unroll
+            for (int i = 0; i < Words<NG>::kRegs; ++i)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) big = __vmaxu2(big, sv[k >> 1][k & 1].u[i] & 0x7fff7fffu);
+            big = max(big & 0xffffu, big >> 16);
+            bool grow = static_cast<int>(big >> 7) - 126 > e_ref;
             float top[NT][2];
 #pragma unroll
             for (int t = 0; t < NT; ++t)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    float mx = kNegInf;
-#pragma unroll
-                    for (int kt = 0; kt < 2; ++kt)
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const int key = key0 + kt * 16 + h * 8 + key_of(r);
-                            const bool seen = key <= hi_key[t][e] && key >= lo_key[t][e] && ((in >> kt) & 1u);
-                            float& z = s[kt][t][h * 2 + e];
-                            z = seen ? z * fac[t][e] : kNegInf;
-                            mx = fmaxf(mx, z);
-                        }
-                    top[t][e] = mx;
-                    grow |= mx > m_ref[t][e] + kLazy;
+                    top[t][e] = fmaxf(fa::ptx::fmax3(s[0][t][e], s[0][t][2 + e], s[1][t][e]), s[1][t][2 + e]);
+                    grow |= top[t][e] > thr[t][e];
                 }
-            // V's scales, zero where the key was not copied or lies past the
-            // sequence (there may be anything there, NaN included)
-            Words<NG> sv[2][2];
-            uint32_t big = 0;
-#pragma unroll
-            for (int kt = 0; kt < 2; ++kt)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int kk = kt * 16 + h * 8 + key_of(r);
-                    sv[kt][h].load(st + 2 * Tile<NG>::kCodes + Tile<NG>::kScales + kk * 2 * NG);
-                    const bool there = key0 + kk < w.len && ((in >> kt) & 1u);
-#pragma unroll
-                    for (int g = 0; g < NG; ++g) {
-                        if (!there) sv[kt][h].w[g] = 0;
-                        big = max(big, static_cast<uint32_t>(sv[kt][h].w[g]) & 0x7fffu);
-                    }
-                }
-            // s < 2^(exponent + 1); the bound moves by one more than it has to
-            grow |= static_cast<int>(big >> 7) - 126 > e_ref || big >= 0x7f80u;   // or a scale is a NaN
             if (__any_sync(0xffffffffu, grow)) {
                 // A NaN scale of V makes its group NaN for the rows that see
                 // the key (whatever p is) and must not reach the others, whose
@@ -488,7 +605,7 @@ __global__ void __launch_bounds__(kWarps * 32) decode_kernel(Cache c, Attend a) 
                                 for (int h = 0; h < 2; ++h)
 #pragma unroll
                                     for (int g = 0; g < NG; ++g)
-                                        if ((sv[kt][h].w[g] & 0x7fffu) >= 0x7f80u && !(s[kt][t][h * 2 + e] == kNegInf))
+                                        if ((sv[kt][h].get(g) & 0x7fffu) >= 0x7f80u && !(s[kt][t][h * 2 + e] == kNegInf))
                                             hit |= 1u << g;
                             hit |= __shfl_xor_sync(0xffffffffu, hit, 4);
                             hit |= __shfl_xor_sync(0xffffffffu, hit, 8);
@@ -507,18 +624,15 @@ __global__ void __launch_bounds__(kWarps * 32) decode_kernel(Cache c, Attend a) 
                         for (int h = 0; h < 2; ++h)
 #pragma unroll
                             for (int g = 0; g < NG; ++g)
-                                if ((sv[kt][h].w[g] & 0x7fffu) >= 0x7f80u) sv[kt][h].w[g] = 0;
+                                if ((sv[kt][h].get(g) & 0x7fffu) >= 0x7f80u) sv[kt][h].set(g, 0);
                 }
                 uint32_t fin = 0;   // the largest scale
 #pragma unroll
-                for (int kt = 0; kt < 2; ++kt)
+                for (int i = 0; i < Words<NG>::kRegs; ++i)
 #pragma unroll
-                    for (int h = 0; h < 2; ++h)
-#pragma unroll
-                        for (int g = 0; g < NG; ++g) {
-                            fin = max(fin, static_cast<uint32_t>(sv[kt][h].w[g]) & 0x7fffu);
-                        }
-                fin = __reduce_max_sync(0xffffffffu, fin);
+                    for (int k = 0; k < 4; ++k) fin = __vmaxu2(fin, sv[k >> 1][k & 1].u[i] & 0x7fff7fffu);
+                fin = __reduce_max_sync(0xffffffffu, max(fin & 0xffffu, fin >> 16));
+                // s < 2^(exponent + 1); the bound moves by one more than it has to
                 const int need = static_cast<int>(fin >> 7) - 126;
                 const int e_new = need > e_ref ? min(need + 1, 128) : e_ref;
                 const float de = fa::ptx::ex2_approx(static_cast<float>(e_ref - e_new));
@@ -531,9 +645,11 @@ __global__ void __launch_bounds__(kWarps * 32) decode_kernel(Cache c, Attend a) 
                         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
                         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
                         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-                        const float mn = fmaxf(m_ref[t][e], mx);
+                        const float mn = fmaxf(m_ref[t][e], mx * fac[t][e]);
                         const float al = (mn == kNegInf ? 1.f : fa::ptx::ex2_approx(m_ref[t][e] - mn)) * de;
                         m_ref[t][e] = mn;
+                        thr[t][e] = (mn + kLazy) / fac[t][e];
+                        neg_ref[t][e] = static_cast<float>(kHead - e_ref) - (mn == kNegInf ? 0.f : mn);
                         l_sum[t][e] *= al;
 #pragma unroll
                         for (int g = 0; g < NG; ++g) {
@@ -546,21 +662,16 @@ __global__ void __launch_bounds__(kWarps * 32) decode_kernel(Cache c, Attend a) 
             }
 
             // ---- p 2^(kHead - E)
-            const float lift = static_cast<float>(kHead - e_ref);
 #pragma unroll
             for (int t = 0; t < NT; ++t)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const float ref = (m_ref[t][e] == kNegInf ? 0.f : m_ref[t][e]) - lift;
+                for (int e = 0; e < 2; ++e)
 #pragma unroll
-                    for (int kt = 0; kt < 2; ++kt)
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            float& z = s[kt][t][h * 2 + e];
-                            z = fa::ptx::ex2_approx(z - ref);
-                            l_sum[t][e] += z;
-                        }
-                }
+                    for (int k = 0; k < 4; ++k) {
+                        float& z = s[k >> 1][t][(k & 1) * 2 + e];
+                        z = fa::ptx::ex2_approx(fmaf(z, fac[t][e], neg_ref[t][e]));
+                        l_sum[t][e] += z;
+                    }
 
             // ---- O^T += V^T P^T
 #pragma unroll
@@ -574,40 +685,42 @@ __global__ void __launch_bounds__(kWarps * 32) decode_kernel(Cache c, Attend a) 
                 }
 #pragma unroll
                 for (int g = 0; g < NG; ++g) {
-                    const uint32_t xa = static_cast<uint32_t>(v[0].w[g]) | (static_cast<uint32_t>(v[1].w[g]) << 16);
-                    const uint32_t xb = static_cast<uint32_t>(v[2].w[g]) | (static_cast<uint32_t>(v[3].w[g]) << 16);
-                    // n - 8 (bits 0..3) and 16 (n - 8) (bits 4..7) in fp16
-                    auto low = [](uint32_t u) {
-                        const uint32_t y = (u & 0x000f000fu) | 0x64006400u;
-                        const __half2 z = __hsub2(*reinterpret_cast<const __half2*>(&y), __half2half2(__ushort_as_half(0x6408)));
-                        return *reinterpret_cast<const uint32_t*>(&z);
-                    };
-                    auto high = [](uint32_t u) {
-                        const uint32_t y = (u & 0x00f000f0u) | 0x64006400u;
-                        const __half2 z = __hsub2(*reinterpret_cast<const __half2*>(&y), __half2half2(__ushort_as_half(0x6480)));
-                        return *reinterpret_cast<const uint32_t*>(&z);
-                    };
-                    const uint32_t a01[4] = {low(xa), high(xa), low(xb), high(xb)};
-                    const uint32_t a23[4] = {low(xa >> 8), high(xa >> 8), low(xb >> 8), high(xb >> 8)};
-                    const float f0 = bf16_bits(sv[kt][0].w[g]), f1 = bf16_bits(sv[kt][1].w[g]);
+                    const uint32_t xa = join_words(v[0], g, v[1], g), xb = join_words(v[2], g, v[3], g);
+                    const uint32_t a01[4] = {low_codes(xa), high_codes(xa), low_codes(xb), high_codes(xb)};
+                    const uint32_t a23[4] = {low_codes(xa >> 8), high_codes(xa >> 8), low_codes(xb >> 8),
+                                             high_codes(xb >> 8)};
+                    const float f0 = sv[kt][0].bf16(g), f1 = sv[kt][1].bf16(g);
 #pragma unroll
                     for (int t = 0; t < NT; ++t) {
-                        const uint32_t b0 = transpose8x8(pack16<false>(s[kt][t][0] * f0, s[kt][t][1] * f0));
-                        const uint32_t b1 = transpose8x8(pack16<false>(s[kt][t][2] * f1, s[kt][t][3] * f1));
+                        const float p0 = s[kt][t][0] * f0, p1 = s[kt][t][1] * f0;
+                        const float p2 = s[kt][t][2] * f1, p3 = s[kt][t][3] * f1;
+                        const uint32_t h0 = pack16<false>(p0, p1), h1 = pack16<false>(p2, p3);
+                        const uint32_t b0 = transpose8x8(h0), b1 = transpose8x8(h1);
                         mma16816(acc[t][g][0], a01, b0, b1);
                         mma16816(acc[t][g][1], a23, b0, b1);
+                        if constexpr (!BF16) {
+                            // fp16 results are held to 2^-12: what P's rounding leaves goes in as well
+                            const float2 q0 = to_f32x2<false>(h0), q1 = to_f32x2<false>(h1);
+                            const uint32_t r0 = transpose8x8(pack16<false>(p0 - q0.x, p1 - q0.y));
+                            const uint32_t r1 = transpose8x8(pack16<false>(p2 - q1.x, p3 - q1.y));
+                            mma16816(acc[t][g][0], a01, r0, r1);
+                            mma16816(acc[t][g][1], a23, r0, r1);
+                        }
                     }
                 }
             }
             __syncwarp();
-            issue(stage);
-            if (++stage == kStages) {
-                stage = 0;
-                parity ^= 1u;
-            }
+#pragma unroll
+            for (int i = 0; i + 1 < kStages; ++i) there[i] = there[i + 1];
+            there[kStages - 1] = copier.copy(c, a, R, run_shift, st);
+            stage = stage + 1 == kStages ? 0 : stage + 1;
         }
 
-        // ---- join the warps
+        // ---- the item's end: its result, or a part to be joined.  Sums are in
+        // units of 2^(m - kHead + E).
+        const bool whole = seg.blk == 0 && seg_blocks == w.blocks;
+        const int part = seg.blk == 0 ? 1 : 0;
+        float* dst = part == 0 ? join + warp * kPart : reinterpret_cast<float*>(ring + warp * kStages * kStage);
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -617,60 +730,79 @@ __global__ void __launch_bounds__(kWarps * 32) decode_kernel(Cache c, Attend a) 
                 l += __shfl_xor_sync(0xffffffffu, l, 4);
                 l += __shfl_xor_sync(0xffffffffu, l, 8);
                 l += __shfl_xor_sync(0xffffffffu, l, 16);
-                // sums are in units of 2^(m - kHead + E)
-                if (r == 0)
-                    join_ml[warp * R + rr] = make_float2(
-                        m_ref[t][e] == kNegInf ? kNegInf : m_ref[t][e] - static_cast<float>(kHead - e_ref), l);
-                float* dst = join + (warp * R + rr) * (D + 4) + 4 * r;
+                const float m = m_ref[t][e] == kNegInf ? kNegInf : -neg_ref[t][e];
+                if (whole) {
+                    if (rr < rows) {
 #pragma unroll
-                for (int g = 0; g < NG; ++g)
-                    *reinterpret_cast<float4*>(dst + g * kGroup) =
-                        make_float4(acc[t][g][0][e], acc[t][g][0][2 + e] * 0.0625f, acc[t][g][1][e],
-                                    acc[t][g][1][2 + e] * 0.0625f);
+                        for (int g = 0; g < NG; ++g)
+                            write_row<BF16>(c, a, w, seg.b, D, tile * R + rr, head, g * kGroup + 4 * r,
+                                            make_float4(acc[t][g][0][e], acc[t][g][0][2 + e] * 0.0625f,
+                                                        acc[t][g][1][e], acc[t][g][1][2 + e] * 0.0625f),
+                                            m, l, g == 0 && r == 0 && a.lse != nullptr);
+                    }
+                } else {
+                    if (r == 0) join_ml[(warp * 2 + part) * R + rr] = make_float2(m, l);
+#pragma unroll
+                    for (int g = 0; g < NG; ++g)
+                        *reinterpret_cast<float4*>(dst + rr * (D + 4) + g * kGroup + 4 * r) =
+                            make_float4(acc[t][g][0][e], acc[t][g][0][2 + e] * 0.0625f, acc[t][g][1][e],
+                                        acc[t][g][1][2 + e] * 0.0625f);
+                }
             }
-        __syncthreads();
-        const bool whole = seg.blk == 0 && seg_hi - seg_lo == w.blocks;
-        const int slot = blockIdx.x * 2 + (seg.blk == 0 ? 1 : 0);
+        if (!whole && lane == 0) parts[warp * 2 + part] = {seg.b, seg.item, seg.blk + seg_blocks == w.blocks};
+        x += seg_blocks;
+        seg.blk += seg_blocks;
+        if (x < x_end) seg.settle(c, a, R);
+    }
+
+    // ---- join the warps' parts.  Those of one item follow one another; a group
+    // that starts and ends its item is the result, else it goes to the
+    // CTA's slot 0 (carries an item on) or 1 (starts one).
+    __syncthreads();
+    for (int p = 0; p < 2 * kWarps;) {
+        const Part first = parts[p];
+        if (first.b < 0) {
+            ++p;
+            continue;
+        }
+        int end = p + 1, last = p;
+        while (end < 2 * kWarps && (parts[end].b < 0 || (parts[end].b == first.b && parts[end].item == first.item))) {
+            if (parts[end].b >= 0) last = end;
+            ++end;
+        }
+        const Work w = work_of(c, a, first.b, R, false);
+        const int head = first.item / w.tiles, tile = first.item - head * w.tiles;
+        const int rows = min(R, w.n * a.G - tile * R);
+        const bool starts = (p & 1) != 0, whole = starts && parts[last].ends;
+        const int slot = blockIdx.x * 2 + (starts ? 1 : 0);
         for (int i = tid; i < rows * (D / 4); i += kWarps * 32) {
             const int rr = i / (D / 4), d4 = i - rr * (D / 4);
-            float2 ml[kWarps];
             float m = kNegInf;
-#pragma unroll
-            for (int k = 0; k < kWarps; ++k) {
-                ml[k] = join_ml[k * R + rr];
-                m = fmaxf(m, ml[k].x);
-            }
+            for (int k = p; k <= last; ++k)
+                if (parts[k].b >= 0) m = fmaxf(m, join_ml[k * R + rr].x);
             float l = 0.f;
             float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-            for (int k = 0; k < kWarps; ++k) {
-                const float f = ml[k].x == kNegInf ? 0.f : fa::ptx::ex2_approx(ml[k].x - m);
-                l += f * ml[k].y;
-                const float4 v = *reinterpret_cast<const float4*>(join + (k * R + rr) * (D + 4) + 4 * d4);
+            for (int k = p; k <= last; ++k) {
+                if (parts[k].b < 0) continue;
+                const float2 ml = join_ml[k * R + rr];
+                const float f = ml.x == kNegInf ? 0.f : fa::ptx::ex2_approx(ml.x - m);
+                const float* src = (k & 1) ? reinterpret_cast<const float*>(ring + (k >> 1) * kStages * kStage)
+                                           : join + (k >> 1) * kPart;
+                const float4 v = *reinterpret_cast<const float4*>(src + rr * (D + 4) + 4 * d4);
+                l += f * ml.y;
                 o.x += f * v.x;
                 o.y += f * v.y;
                 o.z += f * v.z;
                 o.w += f * v.w;
             }
             if (whole) {
-                const int rho = tile * R + rr, qi = rho / a.G, h = head * a.G + rho % a.G;
-                const float inv = l == 0.f ? 0.f : 1.f / l;
-                uint16_t* dst = static_cast<uint16_t*>(a.o) +
-                                (static_cast<long long>(w.row0 + qi) * a.H + h) * D + 4 * d4;
-                *reinterpret_cast<uint2*>(dst) =
-                    make_uint2(pack16<BF16>(o.x * inv, o.y * inv), pack16<BF16>(o.z * inv, o.w * inv));
-                if (a.lse != nullptr && d4 == 0)
-                    a.lse[(c.cu != nullptr ? w.row0 : seg.b * a.lse_batch) + h * a.lse_head + qi] =
-                        l == 0.f ? kNegInf : (m + log2f(l)) * 0.6931471805599453f;
+                write_row<BF16>(c, a, w, first.b, D, tile * R + rr, head, 4 * d4, o, m, l, d4 == 0 && a.lse != nullptr);
             } else {
                 *reinterpret_cast<float4*>(a.part_o + (static_cast<long long>(slot) * R + rr) * D + 4 * d4) = o;
                 if (d4 == 0) a.part_ml[slot * R + rr] = make_float2(m, l);
             }
         }
-        __syncthreads();
-        seg.blk += static_cast<int>(seg_hi - seg_lo);
-        seg_lo = seg_hi;
-        if (seg_lo < hi) seg.settle(c, a, R);
+        p = end;
     }
 }
 
@@ -713,7 +845,7 @@ __global__ void __launch_bounds__(kWarps * 32) combine_kernel(Cache c, Attend a,
             before += two[1][i];
         }
     }
-    const long long quota = max((all + a.grid - 1) / a.grid, static_cast<long long>(kWarps));
+    const long long quota = quota_of(all, a.grid);
     const long long s = before + static_cast<long long>(item) * w.blocks, e = s + w.blocks;
     const int first = static_cast<int>(s / quota), last = static_cast<int>((e - 1) / quota);
     fa::ptx::grid_dependency_wait();
@@ -740,14 +872,7 @@ __global__ void __launch_bounds__(kWarps * 32) combine_kernel(Cache c, Attend a,
             o.z = o.z * f0 + v.z * f1;
             o.w = o.w * f0 + v.w * f1;
         }
-        const int rho = tile * R + rr, qi = rho / a.G, h = head * a.G + rho % a.G;
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-        uint16_t* dst = static_cast<uint16_t*>(a.o) + (static_cast<long long>(w.row0 + qi) * a.H + h) * D + 4 * d4;
-        *reinterpret_cast<uint2*>(dst) =
-            make_uint2(pack16<BF16>(o.x * inv, o.y * inv), pack16<BF16>(o.z * inv, o.w * inv));
-        if (a.lse != nullptr && d4 == 0)
-            a.lse[(c.cu != nullptr ? w.row0 : b * a.lse_batch) + h * a.lse_head + qi] =
-                l == 0.f ? kNegInf : (m + log2f(l)) * 0.6931471805599453f;
+        write_row<BF16>(c, a, w, b, D, tile * R + rr, head, 4 * d4, o, m, l, d4 == 0 && a.lse != nullptr);
     }
 }
 

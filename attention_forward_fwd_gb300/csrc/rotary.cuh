@@ -113,23 +113,25 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(Rotary p) {
 #pragma unroll
                     for (int j = 0; j < VEC; ++j) {
                         // pair j: elements 2 j, 2 j + 1 of the 2 VEC
-                        uint16_t& a = 2 * j < VEC ? lo[k].w[(2 * j) % VEC] : hi[k].w[(2 * j) % VEC];
-                        uint16_t& b = 2 * j + 1 < VEC ? lo[k].w[(2 * j + 1) % VEC] : hi[k].w[(2 * j + 1) % VEC];
-                        const float2 f = kv4::to_f32x2<BF16>(static_cast<uint32_t>(a) | (static_cast<uint32_t>(b) << 16));
                         const float2 r = w[j];
-                        const uint32_t o = kv4::pack16<BF16>(f.x * r.x - f.y * r.y, f.y * r.x + f.x * r.y);
-                        a = static_cast<uint16_t>(o);
-                        b = static_cast<uint16_t>(o >> 16);
+                        if constexpr (VEC == 1) {
+                            const float2 f = kv4::to_f32x2<BF16>(kv4::join_words(lo[k], 0, hi[k], 0));
+                            const uint32_t o = kv4::pack16<BF16>(f.x * r.x - f.y * r.y, f.y * r.x + f.x * r.y);
+                            lo[k].u[0] = o & 0xffffu;
+                            hi[k].u[0] = o >> 16;
+                        } else {
+                            uint32_t& u = j < VEC / 2 ? lo[k].u[j % (VEC / 2)] : hi[k].u[j % (VEC / 2)];
+                            const float2 f = kv4::to_f32x2<BF16>(u);
+                            u = kv4::pack16<BF16>(f.x * r.x - f.y * r.y, f.y * r.x + f.x * r.y);
+                        }
                     }
                 } else {
 #pragma unroll
-                    for (int j = 0; j < VEC; ++j) {
-                        const float2 f = kv4::to_f32x2<BF16>(static_cast<uint32_t>(lo[k].w[j]) |
-                                                             (static_cast<uint32_t>(hi[k].w[j]) << 16));
-                        const float2 r = w[j];
-                        const uint32_t o = kv4::pack16<BF16>(f.x * r.x - f.y * r.y, f.y * r.x + f.x * r.y);
-                        lo[k].w[j] = static_cast<uint16_t>(o);
-                        hi[k].w[j] = static_cast<uint16_t>(o >> 16);
+                    for (int j = 0; j < (VEC + 1) / 2; ++j) {   // pairs 2 j and 2 j + 1
+                        const float2 x = kv4::to_f32x2<BF16>(lo[k].u[j]), y = kv4::to_f32x2<BF16>(hi[k].u[j]);
+                        const float2 r0 = w[2 * j], r1 = VEC > 1 ? w[(2 * j + 1) % VEC] : make_float2(0.f, 0.f);
+                        lo[k].u[j] = kv4::pack16<BF16>(x.x * r0.x - y.x * r0.y, x.y * r1.x - y.y * r1.y);
+                        hi[k].u[j] = kv4::pack16<BF16>(y.x * r0.x + x.x * r0.y, y.y * r1.x + x.y * r1.y);
                     }
                 }
             }

@@ -29,7 +29,7 @@ def bf16_round(x):
 def quantise(x):
     """(codes n in 0..15 as [..., D] uint8, scale bits [..., D / 32]) of rows
     of finite or non-finite float64 values [..., D]."""
-    g = np.asarray(x, np.float64).reshape(*x.shape[:-1], -1, GROUP)
+    g = np.asarray(x, np.float64).reshape(*x.shape[:-1], x.shape[-1] // GROUP, GROUP)
     finite = np.isfinite(g).all(-1)
     safe = np.where(np.isfinite(g), g, 0.0)
     first = np.abs(safe).argmax(-1)                  # argmax: the first of equals

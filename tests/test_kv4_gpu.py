@@ -218,7 +218,7 @@ def run_attention(fa, s, dtype, H, rows, packed, window=-1, scale=None, q16=None
             assert worst <= 1, f"sequence {b} (len {s.lens[b]}, n {n}): |dO| is {worst:.3g} of its bound"
             np.testing.assert_array_equal(np.isneginf(L[:, at]), np.isneginf(rl))
             fin = np.isfinite(rl)
-            worst = (np.abs(L[:, at] - rl)[fin] / tl[fin]).max(initial=0)
+            worst = (np.abs(L[:, at][fin] - rl[fin]) / tl[fin]).max(initial=0)
             assert worst <= 1, f"sequence {b}: |dLSE| is {worst:.3g} of its bound"
             assert (O[at][np.isneginf(rl).T] == 0).all()
     return O, L
@@ -357,12 +357,13 @@ def test_bad_pages_and_lengths_are_reported_and_left_out(fa):
         assert (np.abs(decode(host(o[2]), "bf16") - ro) <= attention_tolerance(
             decode(q16[2], "bf16"), s.rows(2, 0), ro, ra, rl, 0.125, "bf16")[0]).all()
         x = torch.ones(3, 2, 1, 64, dtype=torch.bfloat16, device="cuda")
-        before = c["codes"].clone()
+        before, scales_before = c["codes"].clone(), c["scales"].clone()
         fa.kv4_write(x, x, **c)
         assert fa.fa_device_status(clear=True) == fa.FA_ERR_BAD_PAGES
         own = [int(p) for p in s.table[1] if p >= 0]
         assert torch.equal(before[own], c["codes"][own])
         c["codes"].copy_(before)
+        c["scales"].copy_(scales_before)
 
 
 def test_bad_offsets_are_reported_and_skipped(fa):
@@ -481,7 +482,7 @@ def test_a_graph_follows_the_lengths(fa):
     rows are read on the device."""
     import torch
     s = Setup([30, 47], 1, 64, 16, seed=15)
-    s.table[:, 3] = [s.pages - 1, s.pages - 2]     # the spare pages
+    s.table[0, 2], s.table[1, 3] = s.pages - 1, s.pages - 2     # the spare pages
     c = s.cuda()
     k = torch.zeros(2, 1, 1, 64, dtype=torch.float16, device="cuda")
     v, q = torch.zeros_like(k), torch.zeros(2, 1, 4, 64, dtype=torch.float16, device="cuda")
