@@ -261,72 +261,97 @@ struct Copier {
     Cursor cur;
     int left;              // blocks not copied yet
     int head, item;
-    int page[2];           // of the block at `cur`; -1: nothing to copy
+    int pg, off;           // the block's first key: index into the page table, place in the page
+    int page[2];           // numbers of its pages; they are asked for a block ahead of their use
 
-    // Asks for the pages of the block at `cur`, a block ahead of their use.
-    __device__ __forceinline__ void look_up(const Cache& c, int run_shift) {
+    __device__ __forceinline__ void look_up(const Cache& c) {
         page[0] = page[1] = -1;
         if (left <= 0) return;
+        if (item != cur.item) {   // `copy` sets it to -1 where the sequence may have changed
+            item = cur.item;
+            head = item / cur.w.tiles;
+        }
         const int key0 = cur.w.first + cur.blk * kBlock;
         const int* row = c.table + static_cast<long long>(cur.b) * c.max_pages;
-        if (key0 < cur.w.len) page[0] = __ldg(row + key0 / c.P);
-        if (run_shift == 4 && key0 + 16 < cur.w.len) page[1] = __ldg(row + (key0 + 16) / c.P);
+        if (key0 < cur.w.len) page[0] = __ldg(row + pg);
+        if (key0 + 16 < cur.w.len) page[1] = off + 16 < c.P ? page[0] : __ldg(row + pg + 1);
+    }
+    // The place of the block at `cur`, from scratch.
+    __device__ __forceinline__ void locate(const Cache& c) {
+        const int key0 = cur.w.first + cur.blk * kBlock;
+        pg = key0 / c.P;
+        off = key0 - pg * c.P;
     }
 
     // Copies the block at `cur` to `st` and moves on; bit i of the result: the
     // i-th 16 keys are there.
-    __device__ __forceinline__ uint32_t copy(const Cache& c, const Attend& a, int tile_rows, int run_shift, uint8_t* st) {
+    __device__ __forceinline__ uint32_t copy(const Cache& c, const Attend& a, int tile_rows, uint8_t* st) {
         uint32_t in = 0;
         if (left > 0) {
             const int lane = threadIdx.x & 31;
-            if (item != cur.item) {
-                item = cur.item;
-                head = item / cur.w.tiles;
-            }
             const int key0 = cur.w.first + cur.blk * kBlock;
-            const uint8_t* codes[2];
-            const uint16_t* scales[2];
+            const bool ask0 = key0 < cur.w.len, ask1 = key0 + 16 < cur.w.len;
+            const bool ok0 = ask0 && static_cast<unsigned>(page[0]) < static_cast<unsigned>(c.pages);
+            const bool ok1 = ask1 && static_cast<unsigned>(page[1]) < static_cast<unsigned>(c.pages);
+            if (ask0 != ok0 || ask1 != ok1) report(kStatusBadPages);
+            in = (ok0 ? 1u : 0u) | (ok1 ? 2u : 0u);
+            const uint32_t dst = fa::ptx::smem_addr(st) + lane * 16;
             const long long v_off = static_cast<long long>(c.Hkv) * c.P;   // rows from K to V
+            const long long row0 = (static_cast<long long>(ok0 ? page[0] : 0) * 2 * c.Hkv + head) * c.P + off;
+            if (in == 3u && off + 16 < c.P) {
+                // 32 keys that lie together: 32 NG chunks of 16 bytes of codes, 4 NG of scales
+                const uint8_t* k = c.codes + row0 * (16 * NG) + lane * 16;
+                const uint8_t* v = k + v_off * (16 * NG);
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const bool same = i == 1 && run_shift == 5;
-                const int pg = same ? page[0] : page[i];
-                const bool asked = key0 + 16 * (same ? 0 : i) < cur.w.len;
-                const bool ok = asked && pg >= 0 && pg < c.pages;
-                if (asked && !ok) report(kStatusBadPages);
-                if (ok) in |= 1u << i;
-                const long long row = (static_cast<long long>(ok ? pg : 0) * 2 * c.Hkv + head) * c.P + (key0 + 16 * i) % c.P;
-                codes[i] = c.codes + row * (16 * NG);
-                scales[i] = c.scales + row * NG;
-            }
-            const uint32_t dst = fa::ptx::smem_addr(st);
-            // codes: NG chunks of 16 bytes a key, 32 NG a block
-#pragma unroll
-            for (int i = 0; i < NG; ++i) {
-                const int q = i * 32 + lane;
-                const bool second = q >= 16 * NG;
-                if ((in >> (second ? 1 : 0)) & 1u) {
-                    const uint8_t* src = codes[second ? 1 : 0] + (second ? q - 16 * NG : q) * 16;
-                    copy16(dst + q * 16, src);
-                    copy16(dst + Tile<NG>::kCodes + q * 16, src + v_off * (16 * NG));
+                for (int i = 0; i < NG; ++i) {
+                    copy16(dst + i * 512, k + i * 512);
+                    copy16(dst + Tile<NG>::kCodes + i * 512, v + i * 512);
                 }
-            }
-            // scales: 4 NG chunks a block, K's before V's
+                const uint8_t* ks = reinterpret_cast<const uint8_t*>(c.scales + row0 * NG);
 #pragma unroll
-            for (int i = 0; i < (8 * NG + 31) / 32; ++i) {
-                const int q = i * 32 + lane, which = q >= 4 * NG ? 1 : 0, qq = q - which * 4 * NG;
-                const bool second = qq >= 2 * NG;
-                if (q < 8 * NG && ((in >> (second ? 1 : 0)) & 1u)) {
-                    const uint16_t* src = scales[second ? 1 : 0] + (second ? qq - 2 * NG : qq) * 8 + which * v_off * NG;
-                    copy16(dst + 2 * Tile<NG>::kCodes + q * 16, src);
+                for (int i = 0; i < (8 * NG + 31) / 32; ++i) {
+                    const int q = i * 32 + lane;   // K's, then V's
+                    if (8 * NG % 32 == 0 || q < 8 * NG)
+                        copy16(dst + 2 * Tile<NG>::kCodes + i * 512,
+                               ks + q * 16 + (q >= 4 * NG ? v_off * (2 * NG) - 64 * NG : 0));
+                }
+            } else if (in != 0) {
+                const int off1 = off + 16 < c.P ? off + 16 : 0;
+                const long long row1 = (static_cast<long long>(ok1 ? page[1] : 0) * 2 * c.Hkv + head) * c.P + off1;
+#pragma unroll 1
+                for (int i = 0; i < NG; ++i) {
+                    const int q = i * 32 + lane;
+                    const bool second = q >= 16 * NG;
+                    if ((in >> (second ? 1 : 0)) & 1u) {
+                        const uint8_t* src = c.codes + (second ? row1 : row0) * (16 * NG) + (second ? q - 16 * NG : q) * 16;
+                        copy16(dst + i * 512, src);
+                        copy16(dst + Tile<NG>::kCodes + i * 512, src + v_off * (16 * NG));
+                    }
+                }
+#pragma unroll 1
+                for (int i = 0; i < (8 * NG + 31) / 32; ++i) {
+                    const int q = i * 32 + lane, which = q >= 4 * NG ? 1 : 0, qq = q - which * 4 * NG;
+                    const bool second = qq >= 2 * NG;
+                    if (q < 8 * NG && ((in >> (second ? 1 : 0)) & 1u))
+                        copy16(dst + 2 * Tile<NG>::kCodes + i * 512,
+                               c.scales + ((second ? row1 : row0) + which * v_off) * NG + (second ? qq - 2 * NG : qq) * 8);
                 }
             }
             --left;
             ++cur.blk;
-            if (left > 0) cur.settle(c, a, tile_rows);
+            off += kBlock;
+            while (off >= c.P) {
+                off -= c.P;
+                ++pg;
+            }
+            if (left > 0 && cur.blk >= cur.w.blocks) {
+                cur.settle(c, a, tile_rows);
+                item = -1;
+                locate(c);
+            }
         }
         copies_commit();
-        look_up(c, run_shift);
+        look_up(c);
         return in;
     }
 };
@@ -395,16 +420,16 @@ __global__ void __launch_bounds__(kThreads, NG <= 4 && NT == 1 ? 3 : 2) decode_k
     __syncwarp();
     seg.blk += x;
     if (x < x_end) seg.settle(c, a, R);
-    const int run_shift = (c.P % kBlock) == 0 ? 5 : 4;
     Copier<NG> copier;
     copier.cur = seg;
     copier.left = x_end - x;
     copier.head = 0;
     copier.item = -1;
-    copier.look_up(c, run_shift);
+    copier.locate(c);
+    copier.look_up(c);
     uint32_t there[kStages];
 #pragma unroll
-    for (int i = 0; i < kStages; ++i) there[i] = copier.copy(c, a, R, run_shift, my_ring + i * kStage);
+    for (int i = 0; i < kStages; ++i) there[i] = copier.copy(c, a, R, my_ring + i * kStage);
     int stage = 0;
     const uint16_t* q16 = static_cast<const uint16_t*>(a.q);
 
@@ -712,7 +737,7 @@ __global__ void __launch_bounds__(kThreads, NG <= 4 && NT == 1 ? 3 : 2) decode_k
             __syncwarp();
 #pragma unroll
             for (int i = 0; i + 1 < kStages; ++i) there[i] = there[i + 1];
-            there[kStages - 1] = copier.copy(c, a, R, run_shift, st);
+            there[kStages - 1] = copier.copy(c, a, R, st);
             stage = stage + 1 == kStages ? 0 : stage + 1;
         }
 
