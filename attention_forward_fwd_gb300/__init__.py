@@ -117,7 +117,7 @@ def _declare(lib: ctypes.CDLL) -> ctypes.CDLL:
     lib.fa_fwd_dropout.restype = i
     lib.fa_selftest_timeout.restype = i
     # cache, K, V, k_strides, v_strides, K_out, V_out, dtype, stream
-    cache, ll3 = ctypes.POINTER(Kv4Cache), ctypes.POINTER(ctypes.c_longlong)
+    cache = ll3 = vp   # a Kv4Cache, an array of long long: by reference, or their bytes
     lib.fa_kv4_write.argtypes = [cache, vp, vp, ll3, ll3, vp, vp, i, vp]
     lib.fa_kv4_read.argtypes = [cache, vp, vp, i, vp]
     lib.fa_kv4_attention_workspace_size.argtypes = [cache, i, i, ctypes.POINTER(ctypes.c_size_t)]

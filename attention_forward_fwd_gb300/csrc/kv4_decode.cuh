@@ -13,17 +13,16 @@
 // clock, so the unpacking is what has to be cheap:
 //  * Keys are the M side of both products: one m16n8k16 eats 256 codes for 8
 //    query rows (with the queries on the M side it would eat 128).
-//  * K's codes go to the tensor cores as fp16 subnormals: in bits 4..7 of a half
-//    the nibble n IS n 2^-20, so a pair of codes costs an AND and a shift. The
-//    accumulator of a group starts at -8 sum(q) 2^-20, which turns n into n - 8,
-//    and each group's product is scaled by the key's fp32 scale as it is added up.
-//    (Bits 0..3 would need fewer shifts, but the tensor cores align a subnormal by
-//    its exponent field, and n 2^-24 has 10 bits of nothing in front: results were
-//    off by 2^-14 of a code.)
-//  * V's codes are paired over two keys (one byte permutation); (x & mask | 0x6400)
-//    minus 1032 or 1152 is n - 8 or 16 (n - 8) in fp16, a normal number.  The
-//    offset comes off here, because the accumulator runs over the whole context
-//    and would carry an offset many times the result.
+//  * Codes go to the tensor cores as fp16 integers: (x & mask | 0x6400) minus
+//    1032 or 1152 is n - 8 or 16 (n - 8), exactly, two codes at a time; V's are
+//    paired over two keys by a byte permutation, K's over two runs of 4 elements.
+//    (Subnormals, n 2^-24 or n 2^-20 by a mask alone, would save the
+//    subtraction; but the tensor cores align them by their exponent field, with up
+//    to 10 bits of nothing in front: results off by 2^-14 of a code.  Taking
+//    the offset 8 off the end result loses bits too: V's accumulator runs over
+//    the whole context and would carry an offset many times the result.)
+//  * Each group's part of a score is scaled by the key's fp32 scale as it is
+//    added up, so nothing of K is rounded.
 //  * The scale of V belongs to (key, group): it multiplies P, one fp16 matrix
 //    operand for each group, turned from the accumulator's layout to the
 //    operand's by movmatrix.
@@ -440,9 +439,10 @@ __global__ void __launch_bounds__(kThreads, NG <= 4 && NT == 1 ? 3 : 2) decode_k
         const int head = seg.item / w.tiles, tile = seg.item - head * w.tiles;
         const int rows = min(R, w.n * a.G - tile * R);
 
-        // ---- Q: fp16 with each row's largest magnitude in [2^11, 2^12)
+        // ---- Q: fp16 with each row's largest magnitude in [2^11, 2^12), the
+        // elements that meet codes in bits 4..7 divided by 16
         uint32_t qf[NT][NG][4];
-        float cinit[NT][NG][2], fac[NT][2];
+        float fac[NT][2];
         int hi_key[NT][2], lo_key[NT][2];
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
@@ -473,33 +473,24 @@ __global__ void __launch_bounds__(kThreads, NG <= 4 && NT == 1 ? 3 : 2) decode_k
             // 2^up brings `most` to [2^11, 2^12)
             int up = most > 0.f ? 138 - static_cast<int>((__float_as_uint(most) >> 23) & 255u) : 0;
             up = max(-90, min(100, up));
-            const float mul = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
-            float qsum[NG];
+            const float mul = __uint_as_float(static_cast<uint32_t>(127 + up) << 23), mul16 = mul * 0.0625f;
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
-                // elements 8 cc + e: e = j and 4 + j pair up
+                // elements 8 cc + e: e = j and 4 + j pair up; j odd sits in bits 4..7
                 const float2 e01 = to_f32x2<BF16>(raw[g].x), e23 = to_f32x2<BF16>(raw[g].y);
                 const float2 e45 = to_f32x2<BF16>(raw[g].z), e67 = to_f32x2<BF16>(raw[g].w);
                 qf[t][g][0] = pack16<false>(e01.x * mul, e45.x * mul);       // j = 0
                 qf[t][g][1] = pack16<false>(e23.x * mul, e67.x * mul);       // j = 2
-                qf[t][g][2] = pack16<false>(e01.y * mul, e45.y * mul);       // j = 1
-                qf[t][g][3] = pack16<false>(e23.y * mul, e67.y * mul);       // j = 3
-                const float2 s0 = to_f32x2<false>(qf[t][g][0]), s1 = to_f32x2<false>(qf[t][g][1]);
-                const float2 s2 = to_f32x2<false>(qf[t][g][2]), s3 = to_f32x2<false>(qf[t][g][3]);
-                qsum[g] = ((s0.x + s0.y) + (s1.x + s1.y)) + ((s2.x + s2.y) + (s3.x + s3.y));
-                qsum[g] += __shfl_xor_sync(0xffffffffu, qsum[g], 1);
-                qsum[g] += __shfl_xor_sync(0xffffffffu, qsum[g], 2);
-                qsum[g] *= -8.f * 9.5367431640625e-7f;                       // -8 2^-20
+                qf[t][g][2] = pack16<false>(e01.y * mul16, e45.y * mul16);   // j = 1
+                qf[t][g][3] = pack16<false>(e23.y * mul16, e67.y * mul16);   // j = 3
             }
-            // z = S 2^20 2^-up scale log2 e
-            const float f = fmaxf(a.scale * 1.4426950408889634f * 1048576.f *
+            // z = S 2^-up scale log2 e
+            const float f = fmaxf(a.scale * 1.4426950408889634f *
                                       __uint_as_float(static_cast<uint32_t>(127 - up) << 23), 1.17549435e-38f);
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int from = (2 * cc + e) * 4;   // a lane that holds row 2 cc + e
                 fac[t][e] = __shfl_sync(0xffffffffu, f, from);
-#pragma unroll
-                for (int g = 0; g < NG; ++g) cinit[t][g][e] = __shfl_sync(0xffffffffu, qsum[g], from);
                 // rows past the tile's last one see everything; nobody reads what comes of them
                 const int rr = t * 8 + 2 * cc + e;
                 const int pos = w.len - w.n + (tile * R + rr) / a.G;
@@ -553,13 +544,12 @@ __global__ void __launch_bounds__(kThreads, NG <= 4 && NT == 1 ? 3 : 2) decode_k
                     // r = 2 cc below r = 2 cc + 1
                     const uint32_t x0 = join_words(c0, g, c0, NG + g), x1 = join_words(c1, g, c1, NG + g);
                     const uint32_t y0 = x0 >> 8, y1 = x1 >> 8;
-                    // shifts to the left as products: the FMA pipe has room, the ALU has not
-                    const uint32_t a_even[4] = {(x0 * 16u) & kMid, (x1 * 16u) & kMid, (y0 * 16u) & kMid, (y1 * 16u) & kMid};
-                    const uint32_t a_odd[4] = {x0 & kMid, x1 & kMid, y0 & kMid, y1 & kMid};
+                    const uint32_t a_even[4] = {low_codes(x0), low_codes(x1), low_codes(y0), low_codes(y1)};
+                    const uint32_t a_odd[4] = {high_codes(x0), high_codes(x1), high_codes(y0), high_codes(y1)};
                     const float f0 = s0.bf16(g), f1 = s1.bf16(g);
 #pragma unroll
                     for (int t = 0; t < NT; ++t) {
-                        float d[4] = {cinit[t][g][0], cinit[t][g][1], cinit[t][g][0], cinit[t][g][1]};
+                        float d[4] = {0.f, 0.f, 0.f, 0.f};
                         mma16816(d, a_even, qf[t][g][0], qf[t][g][1]);
                         mma16816(d, a_odd, qf[t][g][2], qf[t][g][3]);
                         s[kt][t][0] = g == 0 ? f0 * d[0] : fmaf(f0, d[0], s[kt][t][0]);

@@ -95,7 +95,7 @@ def _cache(**change):
     d = dict(codes=4096, scales=8192, page_table=4096, seq_lens=4096, cu_seqlens=None, B=2, max_seqlen=3, total=0,
              pages=8, max_pages=4, page_size=32, H_kv=2, D=64)
     d.update(change)
-    return fa.Kv4Cache(**d)
+    return ctypes.byref(fa.Kv4Cache(**d))
 
 
 INV, UNS = fa.FA_ERR_INVALID_ARG, fa.FA_ERR_UNSUPPORTED
