@@ -13,6 +13,7 @@
 #include "fa_kv4_status.h"
 #include "kv4_cache.cuh"
 #include "kv4_decode.cuh"
+#include "kv4_prompt.cuh"
 #include "rotary.cuh"
 
 static_assert(kv4::kStatusTimeout == FA_ERR_TIMEOUT && kv4::kStatusBadSeqlens == FA_ERR_BAD_SEQLENS &&
@@ -155,12 +156,71 @@ int decode(const kv4::Cache& c, kv4::Attend a, void* ws, size_t ws_bytes, Decode
                ? FA_OK : FA_ERR_CUDA;
 }
 
+// Query rows a K/V head (the group's heads times the call's tokens) up to
+// which decode_kernel takes a call.
+constexpr int kDecodeRows = 16;
+
+template <int NG, bool BF16>
+int prompt(const kv4::Cache& c, kv4::Attend a, void* ws, size_t ws_bytes, DecodePlan* only_plan, cudaStream_t st) {
+    using L = kv4::Prompt<NG>;
+    constexpr int R = L::TILES * kv4::kRowTile;
+    static Resident res;
+    auto* kernel = kv4::prompt_kernel<NG, BF16>;
+    int sms = 0, ctas = 0;
+    if (!resident(res, kernel, L::kThreads, L::kSmem, &sms, &ctas)) return FA_ERR_CUDA;
+    kv4::PromptPlan plan;
+    const long long tiles = (static_cast<long long>(c.S) * a.G + R - 1) / R, items = tiles * c.Hkv * c.B;
+    const long long keys = (static_cast<long long>(c.max_pages) * c.P + L::BN - 1) / L::BN;
+    plan.tiles_most = static_cast<int>(tiles);
+    // Items that leave more than half of the SMs idle share their keys out, at
+    // least 4 key tiles to a CTA.
+    plan.splits = static_cast<int>(std::max<long long>(1, std::min<long long>(sms / items, keys / 4)));
+    if (items * plan.splits > 0x7fffffffLL || items * L::TILES * NG > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
+    const size_t slots = plan.splits > 1 ? static_cast<size_t>(items) * plan.splits * R : 0;
+    DecodePlan sizes;
+    sizes.bytes = slots * (L::D * sizeof(float) + sizeof(float2));
+    if (only_plan != nullptr) {
+        *only_plan = sizes;
+        return FA_OK;
+    }
+    if (sizes.bytes > 0 && (ws == nullptr || ws_bytes < sizes.bytes)) return FA_ERR_INVALID_ARG;
+    if (misaligned(ws, 16)) return FA_ERR_UNSUPPORTED;
+    a.part_o = static_cast<float*>(ws);
+    a.part_ml = reinterpret_cast<float2*>(a.part_o + slots * L::D);
+    kernel<<<static_cast<unsigned>(items * plan.splits), L::kThreads, L::kSmem, st>>>(c, a, plan);
+    if (launched() != FA_OK) return FA_ERR_CUDA;
+    if (plan.splits == 1) return FA_OK;
+    cudaLaunchAttribute pdl[1];
+    pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    pdl[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(items * L::TILES * NG));
+    cfg.blockDim = dim3(kv4::kRowTile);
+    cfg.stream = st;
+    cfg.attrs = pdl;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kv4::prompt_combine_kernel<NG, BF16>, c, a, plan) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
 // <groups of a row, tiles of 8 query rows, bf16>
 // Tiles of 16 rows are for D <= 128 only: with D = 256 the accumulators of 16
 // rows would not fit the registers beside the rest.
 int decode_any(int D, bool bf16, const kv4::Cache& c, const kv4::Attend& a, void* ws, size_t ws_bytes,
                DecodePlan* only_plan, cudaStream_t st) {
-    const bool wide = static_cast<long long>(c.S) * a.G > 8;
+    const long long rows = static_cast<long long>(c.S) * a.G;   // numbered with an int
+    if (rows > 0x7fffffffLL - 1024) return FA_ERR_UNSUPPORTED;
+    if (rows > kDecodeRows) {
+#define KV4_ONE(NG_)                                                                              \
+    case NG_:                                                                                     \
+        return bf16 ? prompt<NG_, true>(c, a, ws, ws_bytes, only_plan, st)                        \
+                    : prompt<NG_, false>(c, a, ws, ws_bytes, only_plan, st)
+        switch (D / kv4::kGroup) {
+            KV4_ONE(1); KV4_ONE(2); KV4_ONE(3); KV4_ONE(4); KV4_ONE(5); KV4_ONE(6); KV4_ONE(7); KV4_ONE(8);
+            default: return FA_ERR_UNSUPPORTED;
+        }
+#undef KV4_ONE
+    }
+    const bool wide = rows > 8;
 #define KV4_TWO(NG_)                                                                              \
     case NG_:                                                                                     \
         if (wide && bf16) return decode<NG_, 2, true>(c, a, ws, ws_bytes, only_plan, st);         \

@@ -176,6 +176,21 @@ struct Words {
                 u[i / 2] |= static_cast<uint32_t>(static_cast<const uint16_t*>(p)[i]) << (16 * (i & 1));
         }
     }
+    // the same from memory that nothing writes during the launch
+    __device__ __forceinline__ void load_global(const void* p) {
+        if constexpr (N % 2 == 0) {
+#pragma unroll
+            for (int i = 0; i < N * 2 / static_cast<int>(sizeof(Unit)); ++i) {
+                const Unit v = __ldg(static_cast<const Unit*>(p) + i);
+                __builtin_memcpy(u + i * (sizeof(Unit) / 4), &v, sizeof(Unit));
+            }
+        } else {
+            clear();
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                u[i / 2] |= static_cast<uint32_t>(__ldg(static_cast<const uint16_t*>(p) + i)) << (16 * (i & 1));
+        }
+    }
     __device__ __forceinline__ void store(void* p) const {
         if constexpr (N % 2 == 0) {
 #pragma unroll

@@ -247,6 +247,25 @@ def test_several_tokens(fa, D, H_kv, G, P, n, window):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("D,H_kv,G,P", [(32, 2, 2, 16), (64, 1, 4, 32), (96, 1, 1, 48), (128, 2, 5, 64), (160, 1, 2, 16),
+                                        (192, 2, 1, 32), (224, 1, 3, 16), (256, 1, 4, 128)])
+def test_parts_of_prompts(fa, dtype, D, H_kv, G, P):
+    """More than 16 rows a K/V head, up to several row tiles; the whole
+    sequence, its end, more rows than tokens, nothing cached, nothing at all."""
+    lens, n = [0, 60, 129, 257, 600, 311], 129
+    s = Setup(lens, H_kv, D, P, seed=D + P)
+    run_attention(fa, s, dtype, H_kv * G, [n] * len(lens), packed=False)
+    run_attention(fa, s, dtype, H_kv * G, [0, 60, 129, 257, 17, 1], packed=True, window=100, strided=True)
+
+
+@pytest.mark.parametrize("D,G,n,L", [(128, 4, 20, 9000), (64, 8, 33, 5000), (256, 2, 40, 4000), (96, 1, 150, 6000)])
+def test_prompts_whose_keys_are_shared_out(fa, D, G, n, L):
+    s = Setup([L, L // 3, 5], 1, D, 64, seed=L)
+    run_attention(fa, s, "bf16", G, [n] * 3, packed=False)
+    run_attention(fa, s, "f16", G, [n] * 3, packed=False, window=L // 2)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
 @pytest.mark.parametrize("D,H_kv,G,P", [(128, 2, 4, 32), (64, 1, 2, 16)])
 def test_packed_sequences(fa, dtype, D, H_kv, G, P):
     rows = [1, 0, 4, 1, 90, 2, 0]
@@ -265,50 +284,54 @@ def test_ranges_that_cut_items(fa, B, L, H_kv, G, D, P):
     run_attention(fa, s, "bf16", H_kv * G, [1] * B, packed=False)
 
 
-def test_peaky_scores_and_scales_of_every_size(fa):
+@pytest.mark.parametrize("D,copies", [(64, 1), (64, 10), (160, 1), (160, 10)])
+def test_peaky_scores_and_scales_of_every_size(fa, D, copies):
     """Scores that leave one key, values whose scales differ by 2^40 between
-    tokens, tiny and huge queries."""
-    s = Setup([500], 1, 64, 16, seed=4, loud=1.5)
+    tokens, tiny and huge queries; as a step and as a part of a prompt."""
+    s = Setup([500], 1, D, 16, seed=4, loud=1.5)
     mag = np.exp2(s.r.integers(-20, 21, (500, 1, 1)).astype(float))
-    s.put(0, 1, np.arange(500), s.r.standard_normal((500, 1, 64)) * mag)
-    q = s.r.standard_normal((4, 4, 64)) * np.array([1e-6, 1.0, 20.0, 200.0])[None, :, None]
-    run_attention(fa, s, "bf16", 4, [4], packed=False, q16=to16(q, "bf16"))
+    s.put(0, 1, np.arange(500), s.r.standard_normal((500, 1, D)) * mag)
+    q = s.r.standard_normal((4 * copies, 4, D)) * np.tile([1e-6, 1.0, 20.0, 200.0], copies)[:, None, None]
+    run_attention(fa, s, "bf16", 4, [4 * copies], packed=False, q16=to16(q, "bf16"))
     # one value of scale for the whole call, far from one
     for mag in (2.0 ** -80, 2.0 ** 60):
-        s.put(0, 1, np.arange(500), s.r.standard_normal((500, 1, 64)) * mag)
-        run_attention(fa, s, "bf16", 4, [4], packed=False, q16=to16(q, "bf16"))
-    s.put(0, 1, np.arange(500), np.zeros((500, 1, 64)))
-    O, _ = run_attention(fa, s, "bf16", 4, [4], packed=False, q16=to16(q, "bf16"))
+        s.put(0, 1, np.arange(500), s.r.standard_normal((500, 1, D)) * mag)
+        run_attention(fa, s, "bf16", 4, [4 * copies], packed=False, q16=to16(q, "bf16"))
+    s.put(0, 1, np.arange(500), np.zeros((500, 1, D)))
+    O, _ = run_attention(fa, s, "bf16", 4, [4 * copies], packed=False, q16=to16(q, "bf16"))
     assert (O == 0).all()
 
 
-def test_nan_reaches_its_rows_and_groups_only(fa):
+@pytest.mark.parametrize("D,heads", [(64, 2), (64, 4), (256, 4)])
+def test_nan_reaches_its_rows_and_groups_only(fa, D, heads):
     """A NaN in a key makes the rows that see it NaN, one in a value its group
     of 32 elements; rows that do not see the token stay as they are."""
-    D, n = 64, 8
+    n = 8
     for which in (0, 1):
         s = Setup([70], 1, D, 16, seed=6)
-        q16 = to16(s.r.standard_normal((n, 2, D)), "f16")
-        clean, _ = run_attention(fa, s, "f16", 2, [n], packed=False, q16=q16)
+        q16 = to16(s.r.standard_normal((n, heads, D)), "f16")
+        clean, _ = run_attention(fa, s, "f16", heads, [n], packed=False, q16=q16)
         bad = 66                                     # rows 0 .. 3 are tokens 62 .. 65
         s.scales[s.table[0, bad // 16], which, 0, bad % 16, 1] = 0x7FC0
-        O, L = run_attention(fa, s, "f16", 2, [n], packed=False, q16=q16, check=False)
+        O, L = run_attention(fa, s, "f16", heads, [n], packed=False, q16=q16, check=False)
         np.testing.assert_array_equal(O[:4], clean[:4])
         if which == 0:
             assert np.isnan(O[4:]).all() and np.isnan(L[:, 4:]).all()
         else:
-            assert np.isnan(O[4:, :, 32:]).all()
+            assert np.isnan(O[4:, :, 32:64]).all()
             np.testing.assert_allclose(O[4:, :, :32], clean[4:, :, :32], rtol=2e-3, atol=1e-4)
+            np.testing.assert_allclose(O[4:, :, 64:], clean[4:, :, 64:], rtol=2e-3, atol=1e-4)
 
 
-def test_nan_in_a_query_stays_in_its_row(fa):
+@pytest.mark.parametrize("n", [2, 30])
+def test_nan_in_a_query_stays_in_its_row(fa, n):
     s = Setup([50], 1, 64, 16, seed=7)
-    q16 = to16(s.r.standard_normal((2, 4, 64)), "bf16")
-    clean, cl = run_attention(fa, s, "bf16", 4, [2], packed=False, q16=q16)
+    q16 = to16(s.r.standard_normal((n, 4, 64)), "bf16")
+    clean, cl = run_attention(fa, s, "bf16", 4, [n], packed=False, q16=q16)
     q16[1, 2, 5] = 0x7FC0
     q16[0, 3, 9] = 0x7F80
-    O, L = run_attention(fa, s, "bf16", 4, [2], packed=False, q16=q16, check=False)
-    hit = np.zeros((2, 4), bool)
+    O, L = run_attention(fa, s, "bf16", 4, [n], packed=False, q16=q16, check=False)
+    hit = np.zeros((n, 4), bool)
     hit[1, 2] = hit[0, 3] = True
     assert np.isnan(O[hit]).all() and np.isnan(L.T[hit]).all()
     np.testing.assert_array_equal(O[~hit], clean[~hit])
