@@ -172,11 +172,25 @@ int prompt(const kv4::Cache& c, kv4::Attend a, void* ws, size_t ws_bytes, Decode
     const long long tiles = (static_cast<long long>(c.S) * a.G + R - 1) / R, items = tiles * c.Hkv * c.B;
     const long long keys = (static_cast<long long>(c.max_pages) * c.P + L::BN - 1) / L::BN;
     plan.tiles_most = static_cast<int>(tiles);
-    // Items that leave more than half of the SMs idle share their keys out, at
-    // least 4 key tiles to a CTA.
-    plan.splits = static_cast<int>(std::max<long long>(1, std::min<long long>(sms / items, keys / 4)));
-    if (items * plan.splits > 0x7fffffffLL || items * L::TILES * NG > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
-    const size_t slots = plan.splits > 1 ? static_cast<size_t>(items) * plan.splits * R : 0;
+    // The items behind the last whole wave of CTAs share their keys out so that
+    // the SMs end together: s CTAs an item, each with its share of the key
+    // tiles and about three tiles' time to start and end, and a second launch.
+    const long long whole = items / sms * sms, rest = items - whole;
+    long long best = rest > 0 ? keys + 3 : 0;
+    plan.whole = static_cast<int>(std::min<long long>(items, 0x7fffffff));
+    plan.splits = 1;
+    for (long long s = 2; s <= std::min<long long>(sms, keys / 4) && rest > 0; ++s) {
+        const long long cost = (rest * s + sms - 1) / sms * ((keys + s - 1) / s + 3) + 4;
+        if (cost < best) {
+            best = cost;
+            plan.whole = static_cast<int>(whole);
+            plan.splits = static_cast<int>(s);
+        }
+    }
+    const long long split_items = plan.splits > 1 ? rest : 0;
+    const long long grid = items - split_items + split_items * plan.splits;
+    if (grid > 0x7fffffffLL || items * L::TILES * NG > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
+    const size_t slots = static_cast<size_t>(split_items) * plan.splits * R;
     DecodePlan sizes;
     sizes.bytes = slots * (L::D * sizeof(float) + sizeof(float2));
     if (only_plan != nullptr) {
@@ -187,14 +201,14 @@ int prompt(const kv4::Cache& c, kv4::Attend a, void* ws, size_t ws_bytes, Decode
     if (misaligned(ws, 16)) return FA_ERR_UNSUPPORTED;
     a.part_o = static_cast<float*>(ws);
     a.part_ml = reinterpret_cast<float2*>(a.part_o + slots * L::D);
-    kernel<<<static_cast<unsigned>(items * plan.splits), L::kThreads, L::kSmem, st>>>(c, a, plan);
+    kernel<<<static_cast<unsigned>(grid), L::kThreads, L::kSmem, st>>>(c, a, plan);
     if (launched() != FA_OK) return FA_ERR_CUDA;
     if (plan.splits == 1) return FA_OK;
     cudaLaunchAttribute pdl[1];
     pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     pdl[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(items * L::TILES * NG));
+    cfg.gridDim = dim3(static_cast<unsigned>(split_items * L::TILES * NG));
     cfg.blockDim = dim3(kv4::kRowTile);
     cfg.stream = st;
     cfg.attrs = pdl;

@@ -78,9 +78,12 @@ struct PromptBars {
 };
 static_assert(sizeof(PromptBars) <= 2048, "barriers");
 
+// The items (row tiles of R rows, K/V heads, sequences) in the order of the
+// grid; those of whole waves have a CTA each, those behind them `splits`.
 struct PromptPlan {
-    int tiles_most;        // row tiles (TILES x 128 rows) of a sequence and K/V head
-    int splits;            // CTAs that share an item's keys
+    int tiles_most;        // row tiles of a sequence and K/V head
+    int whole;             // items that are not split
+    int splits;            // CTAs that share the keys of one of the others
 };
 
 // Bounded wait; false (and the CTA's abort flag set) when it ran out, or when
@@ -143,8 +146,10 @@ __global__ void __launch_bounds__(Prompt<NG>::kThreads, 1) prompt_kernel(Cache c
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     // ------------------------------------------------------------ the item
-    const int split = static_cast<int>(blockIdx.x) % plan.splits;
-    const int y = static_cast<int>(blockIdx.x) / plan.splits;
+    const int behind = static_cast<int>(blockIdx.x) - plan.whole;
+    const int splits = behind < 0 ? 1 : plan.splits;
+    const int split = behind < 0 ? 0 : behind % plan.splits;
+    const int y = behind < 0 ? static_cast<int>(blockIdx.x) : plan.whole + behind / plan.splits;
     const int bh = y % (c.B * c.Hkv), b = bh / c.Hkv, head = bh - b * c.Hkv;
     const int tile = plan.tiles_most - 1 - y / (c.B * c.Hkv);    // the longest first
     const Work w = work_of(c, a, b, R, tile == 0 && head == 0 && split == 0 && threadIdx.x == 0);
@@ -154,8 +159,8 @@ __global__ void __launch_bounds__(Prompt<NG>::kThreads, 1) prompt_kernel(Cache c
     const int pos0 = w.len - w.n + tile * R / a.G, pos1 = w.len - w.n + (tile * R + rows - 1) / a.G;
     const int t_lo = a.window >= 0 ? max(0, pos0 - a.window) / BN : 0;
     const int t_all = pos1 >= 0 ? pos1 / BN + 1 - t_lo : 0;
-    const int jb = t_lo + static_cast<int>(static_cast<long long>(t_all) * split / plan.splits);
-    const int n_tiles = t_lo + static_cast<int>(static_cast<long long>(t_all) * (split + 1) / plan.splits) - jb;
+    const int jb = t_lo + static_cast<int>(static_cast<long long>(t_all) * split / splits);
+    const int n_tiles = t_lo + static_cast<int>(static_cast<long long>(t_all) * (split + 1) / splits) - jb;
 
     if (threadIdx.x == 0) {
         fa::ptx::mbar_init(bar(&bars->q_full), R);
@@ -287,10 +292,11 @@ __global__ void __launch_bounds__(Prompt<NG>::kThreads, 1) prompt_kernel(Cache c
             }
         }
         const int* table = c.table + static_cast<long long>(b) * c.max_pages;
-        // raw rows of tile j (zeros where there is no key), asked for a tile ahead
-        Words<2 * NG> kr[CU], vr[CU];
-        Words<NG> ks, vs;
-        bool gone = false;
+        // raw rows of tile j (zeros where there is no key), and of the next one, which is
+        // asked for before this one is unpacked; its page was asked for a tile before that
+        Words<2 * NG> kr[CU], vr[CU], kr2[CU], vr2[CU];
+        Words<NG> ks, vs, ks2, vs2;
+        bool gone = false, gone2 = false;
         int page = -1;
         auto look_up = [&](int j) {
             const int pos = (jb + j) * BN + key;
@@ -300,32 +306,45 @@ __global__ void __launch_bounds__(Prompt<NG>::kThreads, 1) prompt_kernel(Cache c
             const int pos = (jb + j) * BN + key;
             const bool mine = j < n_tiles && pos < w.len;
             const bool ok = mine && page >= 0 && page < c.pages;
-            gone = mine && !ok;
-            if (gone) report(kStatusBadPages);
+            gone2 = mine && !ok;
+            if (gone2) report(kStatusBadPages);
             if (ok) {
                 const long long row = (static_cast<long long>(page) * 2 * c.Hkv + head) * c.P + pos % c.P;
 #pragma unroll
                 for (int i = 0; i < CU; ++i) {
-                    kr[i].load_global(c.codes + row * (16 * NG) + (c0 + i) * (4 * NG));
-                    vr[i].load_global(c.codes + (row + k_to_v) * (16 * NG) + (c0 + i) * (4 * NG));
+                    kr2[i].load_global(c.codes + row * (16 * NG) + (c0 + i) * (4 * NG));
+                    vr2[i].load_global(c.codes + (row + k_to_v) * (16 * NG) + (c0 + i) * (4 * NG));
                 }
-                ks.load_global(c.scales + row * NG);
-                vs.load_global(c.scales + (row + k_to_v) * NG);
+                ks2.load_global(c.scales + row * NG);
+                vs2.load_global(c.scales + (row + k_to_v) * NG);
             } else {
 #pragma unroll
                 for (int i = 0; i < CU; ++i) {
-                    kr[i].clear();
-                    vr[i].clear();
+                    kr2[i].clear();
+                    vr2[i].clear();
                 }
-                ks.clear();
-                vs.clear();
+                ks2.clear();
+                vs2.clear();
             }
+        };
+        auto shift = [&] {
+#pragma unroll
+            for (int i = 0; i < CU; ++i) {
+                kr[i] = kr2[i];
+                vr[i] = vr2[i];
+            }
+            ks = ks2;
+            vs = vs2;
+            gone = gone2;
         };
         look_up(0);
         load(0);
         look_up(1);
         bool ok = true;
         for (int j = 0; j < n_tiles; ++j) {
+            shift();
+            load(j + 1);
+            look_up(j + 2);
             // ---- the tile's largest finite scales, NaNs and holes
             uint32_t kt = 0, vt = 0, nan_groups = 0;
 #pragma unroll
@@ -388,8 +407,6 @@ __global__ void __launch_bounds__(Prompt<NG>::kThreads, 1) prompt_kernel(Cache c
                 __syncwarp();
                 if (lane == 0) fa::ptx::mbar_arrive(bar(&bars->v_full[j & 1]));
             }
-            load(j + 1);
-            look_up(j + 2);
         }
     } else {
         // --------------------------------------------------------- softmax
@@ -451,15 +468,17 @@ __global__ void __launch_bounds__(Prompt<NG>::kThreads, 1) prompt_kernel(Cache c
             const TileInfo info = bars->tile[j % kInfo];
             const uint32_t tS = tmem + lane_off + sb * 128;
             const int kv0 = (jb + j) * BN;
-            const bool edge = kv0 + BN - 1 > pos || kv0 < first || info.missing != 0;
+            const bool edge = __any_sync(0xffffffffu, kv0 + BN - 1 > pos || kv0 < first || info.missing != 0);
             const float zf = f * pow2(info.ek), ev = static_cast<float>(info.ev);
             auto mask = [&](uint32_t* s, int q) {   // columns 32 q .. 32 q + 31
+                // bit k: column k is seen
+                const int from = min(max(first - kv0 - 32 * q, 0), 32), to = min(max(pos - kv0 - 32 * q + 1, 0), 32);
+                uint32_t seen = (to == 32 ? 0xffffffffu : (1u << to) - 1u) & (from == 32 ? 0u : 0xffffffffu << from);
+                if ((info.missing >> (2 * q)) & 1u) seen &= 0xffff0000u;
+                if ((info.missing >> (2 * q)) & 2u) seen &= 0x0000ffffu;
 #pragma unroll
-                for (int k = 0; k < 32; ++k) {
-                    const int key = kv0 + 32 * q + k;
-                    if (key > pos || key < first || ((info.missing >> (2 * q + (k >> 4))) & 1u))
-                        s[k] = __float_as_uint(kNegInf);
-                }
+                for (int k = 0; k < 32; ++k)
+                    if (!((seen >> k) & 1u)) s[k] = __float_as_uint(kNegInf);
             };
             float mx = kNegInf;
 #pragma unroll
@@ -550,8 +569,8 @@ __global__ void __launch_bounds__(Prompt<NG>::kThreads, 1) prompt_kernel(Cache c
         ok = __all_sync(0xffffffffu, ok);
         fa::ptx::tc_fence_after_sync();
         const float m = ref == kNegInf ? kNegInf : ref - kPHead;
-        const long long slot = (static_cast<long long>(y) * plan.splits + split) * TILES + t;
-        if (ok && plan.splits > 1 && real) a.part_ml[slot * kRowTile + r] = make_float2(m, n_tiles > 0 ? l : 0.f);
+        const long long slot = (static_cast<long long>(y - plan.whole) * splits + split) * TILES + t;
+        if (ok && splits > 1 && real) a.part_ml[slot * kRowTile + r] = make_float2(m, n_tiles > 0 ? l : 0.f);
         const float inv = l == 0.f ? 0.f : 1.f / l;
         if (ok) {
 #pragma unroll 1
@@ -576,7 +595,7 @@ __global__ void __launch_bounds__(Prompt<NG>::kThreads, 1) prompt_kernel(Cache c
                                                  __uint_as_float(o[8 * i + 4]), __uint_as_float(o[8 * i + 6]));
                     const float4 g = make_float4(__uint_as_float(o[8 * i + 1]), __uint_as_float(o[8 * i + 3]),
                                                  __uint_as_float(o[8 * i + 5]), __uint_as_float(o[8 * i + 7]));
-                    if (plan.splits > 1) {
+                    if (splits > 1) {
                         float4* po = reinterpret_cast<float4*>(a.part_o) + (slot * (D / 4) + q * 8 + 2 * i) * kRowTile + r;
                         po[0] = e;
                         po[kRowTile] = g;
@@ -589,7 +608,7 @@ __global__ void __launch_bounds__(Prompt<NG>::kThreads, 1) prompt_kernel(Cache c
                     }
                 }
             }
-            if (plan.splits == 1 && real && a.lse != nullptr)
+            if (splits == 1 && real && a.lse != nullptr)
                 a.lse[(c.cu != nullptr ? w.row0 : b * a.lse_batch) + h * a.lse_head + qi] =
                     l == 0.f ? kNegInf : (m + log2f(l)) * 0.6931471805599453f;
         }
@@ -610,7 +629,7 @@ __global__ void __launch_bounds__(kRowTile) prompt_combine_kernel(Cache c, Atten
     constexpr int D = L::D, TILES = L::TILES, R = TILES * kRowTile;
     fa::ptx::grid_dependency_wait();
     const int q = static_cast<int>(blockIdx.x) % NG, yt = static_cast<int>(blockIdx.x) / NG;
-    const int t = yt % TILES, y = yt / TILES;
+    const int t = yt % TILES, y = plan.whole + yt / TILES;
     const int bh = y % (c.B * c.Hkv), b = bh / c.Hkv, head = bh - b * c.Hkv;
     const int tile = plan.tiles_most - 1 - y / (c.B * c.Hkv);
     const Work w = work_of(c, a, b, R, false);
@@ -618,14 +637,14 @@ __global__ void __launch_bounds__(kRowTile) prompt_combine_kernel(Cache c, Atten
     if (tile >= w.tiles || rho >= w.n * a.G) return;
     float m = kNegInf, l = 0.f;
     for (int s = 0; s < plan.splits; ++s) {
-        const long long slot = (static_cast<long long>(y) * plan.splits + s) * TILES + t;
+        const long long slot = (static_cast<long long>(y - plan.whole) * plan.splits + s) * TILES + t;
         m = fmaxf(m, __ldcg(a.part_ml + slot * kRowTile + r).x);
     }
     float4 o[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int s = 0; s < plan.splits; ++s) {
-        const long long slot = (static_cast<long long>(y) * plan.splits + s) * TILES + t;
+        const long long slot = (static_cast<long long>(y - plan.whole) * plan.splits + s) * TILES + t;
         const float2 ml = __ldcg(a.part_ml + slot * kRowTile + r);
         const float f = ml.x == kNegInf ? 0.f : fa::ptx::ex2_approx(ml.x - m);
         l += f * ml.y;
