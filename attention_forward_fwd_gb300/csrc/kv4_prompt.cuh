@@ -7,8 +7,10 @@
 // unpacked K and V), and walks over tiles of BN keys:
 //   unpack warps   codes and scales -> fp16 K and V tiles in shared memory
 //   MMA warp       S_t = Q_t K^T, O_t += P_t V (fp32 in tensor memory)
-//   softmax warps  thread = row = TMEM lane: S -> P (fp16, over S), the
-//                  running maximum, O's rescaling, the row sum
+//   softmax warps  two threads a row (TMEM lane), each with half of the keys:
+//                  S -> P (fp16, over S), the running maximum, O's rescaling,
+//                  the row sum.  (One thread a row takes 3700 cycles a tile,
+//                  nearly twice what the two products of both row tiles take.)
 // D <= 128: two row tiles that take turns on the tensor pipe (S_A, S_B, then
 // P_A V, S_A of the next keys, P_B V, ...).  D > 128: one row tile, as two O
 // tiles do not fit, with two S buffers (S of the next keys runs beside the softmax).
@@ -37,7 +39,6 @@ namespace kv4 {
 
 constexpr int kRowTile = 128;
 constexpr int kInfo = 4;               // tile descriptions in flight
-constexpr int kUnpackWarps = 8;
 constexpr float kPHead = 7.f;          // P is held as p 2^kPHead, p <= 2^kLazy
 
 template <int NG>
@@ -48,13 +49,14 @@ struct Prompt {
     static constexpr int BN = kWide ? 64 : 128;
     static constexpr int kBoxes = (NG + 1) / 2;            // 64 columns each
     static constexpr int N = kBoxes * 64;                  // columns of O (past D: zeros)
-    static constexpr int kSoftWarps = 4 * TILES;
+    static constexpr int kSoftWarps = 8 * TILES;
+    static constexpr int kUnpackWarps = kWide ? 8 : 4;
     static constexpr int kMmaWarp = kSoftWarps + kUnpackWarps;
     static constexpr int kThreads = (kMmaWarp + 1) * 32;
     static constexpr int kQBox = kRowTile * 128, kBox = BN * 128;   // bytes
     static constexpr int kQTile = kBoxes * kQBox, kTile = kBoxes * kBox;
     static constexpr int kOffK = TILES * kQTile, kOffV = kOffK + 2 * kTile, kOffBar = kOffV + 2 * kTile;
-    static constexpr int kSmem = kOffBar + 2048 + 1024;    // and room to align
+    static constexpr int kSmem = kOffBar + 4096 + 1024;    // and room to align
     static constexpr uint32_t kO = 256;                    // TMEM: S at 0 and 128, O from here on
     static_assert(kO + TILES * N <= 512, "tensor memory");
     static_assert(kSmem <= 232448, "shared memory");
@@ -70,13 +72,14 @@ struct PromptBars {
     uint64_t q_full, k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_done, o_last, info[kInfo],
         drain;
     TileInfo tile[kInfo];
-    uint32_t top[2][kUnpackWarps];       // largest scales: K below V
-    uint32_t gone[2][kUnpackWarps];
+    uint32_t top[2][8];                  // of each unpack warp: largest scales, K below V
+    uint32_t gone[2][8];
+    float half_max[2][2][128];           // [row tile][half of the keys][row]
     uint8_t nan_groups[kInfo][128];      // of each key of V
     uint32_t tmem;
     int abort;
 };
-static_assert(sizeof(PromptBars) <= 2048, "barriers");
+static_assert(sizeof(PromptBars) <= 4096, "barriers");
 
 // The items (row tiles of R rows, K/V heads, sequences) in the order of the
 // grid; those of whole waves have a CTA each, those behind them `splits`.
@@ -135,7 +138,7 @@ __global__ void __launch_bounds__(Prompt<NG>::kThreads, 1) prompt_kernel(Cache c
     using L = Prompt<NG>;
     constexpr int D = L::D, TILES = L::TILES, BN = L::BN, NB = L::kBoxes, N = L::N;
     constexpr bool WIDE = L::kWide;
-    constexpr int R = TILES * kRowTile;
+    constexpr int R = TILES * kRowTile, kUnpackWarps = L::kUnpackWarps;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~static_cast<uintptr_t>(1023));
@@ -163,14 +166,14 @@ __global__ void __launch_bounds__(Prompt<NG>::kThreads, 1) prompt_kernel(Cache c
     const int n_tiles = t_lo + static_cast<int>(static_cast<long long>(t_all) * (split + 1) / splits) - jb;
 
     if (threadIdx.x == 0) {
-        fa::ptx::mbar_init(bar(&bars->q_full), R);
+        fa::ptx::mbar_init(bar(&bars->q_full), 2 * R);
         for (int i = 0; i < 2; ++i) {
             fa::ptx::mbar_init(bar(&bars->k_full[i]), kUnpackWarps);
             fa::ptx::mbar_init(bar(&bars->k_empty[i]), 1);
             fa::ptx::mbar_init(bar(&bars->v_full[i]), kUnpackWarps);
             fa::ptx::mbar_init(bar(&bars->v_empty[i]), 1);
             fa::ptx::mbar_init(bar(&bars->s_full[i]), 1);
-            fa::ptx::mbar_init(bar(&bars->p_full[i]), kRowTile);
+            fa::ptx::mbar_init(bar(&bars->p_full[i]), 2 * kRowTile);
         }
         for (int i = 0; i < kInfo; ++i) fa::ptx::mbar_init(bar(&bars->info[i]), 1);
         fa::ptx::mbar_init(bar(&bars->o_done), 1);
@@ -278,7 +281,7 @@ __global__ void __launch_bounds__(Prompt<NG>::kThreads, 1) prompt_kernel(Cache c
         wait_warp(bar(&bars->drain), 0, false);
     } else if (warp >= L::kSoftWarps) {
         // ---------------------------------------------------------- unpack
-        constexpr int CU = BN / 64;                        // 4 units (c = 0 .. 3) a key over 256 threads
+        constexpr int CU = BN * 4 / (kUnpackWarps * 32);   // of the 4 units (c = 0 .. 3) of a key
         const int u = static_cast<int>(threadIdx.x) - L::kSoftWarps * 32;
         const int key = u % BN, c0 = u / BN * CU;          // this thread's units: c0 .. c0 + CU - 1
         const int uw = u >> 5;
@@ -292,59 +295,57 @@ __global__ void __launch_bounds__(Prompt<NG>::kThreads, 1) prompt_kernel(Cache c
             }
         }
         const int* table = c.table + static_cast<long long>(b) * c.max_pages;
-        // raw rows of tile j (zeros where there is no key), and of the next one, which is
-        // asked for before this one is unpacked; its page was asked for a tile before that
-        Words<2 * NG> kr[CU], vr[CU], kr2[CU], vr2[CU];
+        // The rows of tile j + 1 are asked for as those of tile j have been
+        // unpacked (K's latency runs beside V's unpacking and the other way
+        // round), their scales as tile j begins, their page a tile before that.
+        Words<2 * NG> kr[CU], vr[CU];
         Words<NG> ks, vs, ks2, vs2;
+        long long row2 = -1;        // row of the next tile's key in the cache; -1: none
         bool gone = false, gone2 = false;
-        int page = -1;
-        auto look_up = [&](int j) {
-            const int pos = (jb + j) * BN + key;
-            page = j < n_tiles && pos < w.len ? __ldg(table + pos / c.P) : -1;
-        };
-        auto load = [&](int j) {
-            const int pos = (jb + j) * BN + key;
-            const bool mine = j < n_tiles && pos < w.len;
+        int next = jb * BN + key;   // position that `pg`, `off` and `page` stand for
+        int pg = next / c.P, off = next - pg * c.P, page = -1, tile_at = 0;
+        const int step_pg = BN / c.P, step_off = BN - step_pg * c.P;
+        auto look_up = [&] { page = tile_at < n_tiles && next < w.len ? __ldg(table + pg) : -1; };
+        // the page of tile `tile_at` is here: its row, its scales; ask for the next page
+        auto advance = [&] {
+            const bool mine = tile_at < n_tiles && next < w.len;
             const bool ok = mine && page >= 0 && page < c.pages;
             gone2 = mine && !ok;
             if (gone2) report(kStatusBadPages);
+            row2 = ok ? (static_cast<long long>(page) * 2 * c.Hkv + head) * c.P + off : -1;
+            ks2.clear();
+            vs2.clear();
             if (ok) {
-                const long long row = (static_cast<long long>(page) * 2 * c.Hkv + head) * c.P + pos % c.P;
-#pragma unroll
-                for (int i = 0; i < CU; ++i) {
-                    kr2[i].load_global(c.codes + row * (16 * NG) + (c0 + i) * (4 * NG));
-                    vr2[i].load_global(c.codes + (row + k_to_v) * (16 * NG) + (c0 + i) * (4 * NG));
-                }
-                ks2.load_global(c.scales + row * NG);
-                vs2.load_global(c.scales + (row + k_to_v) * NG);
-            } else {
-#pragma unroll
-                for (int i = 0; i < CU; ++i) {
-                    kr2[i].clear();
-                    vr2[i].clear();
-                }
-                ks2.clear();
-                vs2.clear();
+                ks2.load_global(c.scales + row2 * NG);
+                vs2.load_global(c.scales + (row2 + k_to_v) * NG);
             }
+            ++tile_at;
+            next += BN;
+            pg += step_pg;
+            off += step_off;
+            if (off >= c.P) {
+                off -= c.P;
+                ++pg;
+            }
+            look_up();
         };
-        auto shift = [&] {
+        auto load_rows = [&](Words<2 * NG>* to, long long from) {
 #pragma unroll
             for (int i = 0; i < CU; ++i) {
-                kr[i] = kr2[i];
-                vr[i] = vr2[i];
+                to[i].clear();
+                if (from >= 0) to[i].load_global(c.codes + from * (16 * NG) + (c0 + i) * (4 * NG));
             }
+        };
+        look_up();
+        advance();
+        load_rows(kr, row2);
+        load_rows(vr, row2 < 0 ? -1 : row2 + k_to_v);
+        bool ok = true;
+        for (int j = 0; j < n_tiles; ++j) {
             ks = ks2;
             vs = vs2;
             gone = gone2;
-        };
-        look_up(0);
-        load(0);
-        look_up(1);
-        bool ok = true;
-        for (int j = 0; j < n_tiles; ++j) {
-            shift();
-            load(j + 1);
-            look_up(j + 2);
+            advance();
             // ---- the tile's largest finite scales, NaNs and holes
             uint32_t kt = 0, vt = 0, nan_groups = 0;
 #pragma unroll
@@ -397,6 +398,7 @@ __global__ void __launch_bounds__(Prompt<NG>::kThreads, 1) prompt_kernel(Cache c
                 fa::ptx::fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) fa::ptx::mbar_arrive(bar(&bars->k_full[j & 1]));
+                load_rows(kr, row2);
                 if (j >= 2) ok = wait_warp(bar(&bars->v_empty[j & 1]), static_cast<uint32_t>(((j >> 1) - 1) & 1));
             }
             if (ok) {
@@ -406,12 +408,15 @@ __global__ void __launch_bounds__(Prompt<NG>::kThreads, 1) prompt_kernel(Cache c
                 fa::ptx::fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) fa::ptx::mbar_arrive(bar(&bars->v_full[j & 1]));
+                load_rows(vr, row2 < 0 ? -1 : row2 + k_to_v);
             }
         }
     } else {
         // --------------------------------------------------------- softmax
-        const int t = warp >> 2;                                      // row tile
-        const int r = static_cast<int>(threadIdx.x) & 127;            // row of it, TMEM lane
+        constexpr int HALF = BN / 2;
+        const int t = warp >> 3, half = (warp >> 2) & 1;              // row tile, half of its keys
+        const int r = static_cast<int>(threadIdx.x) & 127;            // row of the tile, TMEM lane
+        const uint32_t pair_bar = 4 + t * 4 + (warp & 3);             // this warp and the one with the other half
         const int row = t * kRowTile + r, rho = tile * R + row;
         const bool real = row < rows;
         const int qi = rho / a.G, h = head * a.G + rho - qi * a.G;
@@ -440,8 +445,9 @@ __global__ void __launch_bounds__(Prompt<NG>::kThreads, 1) prompt_kernel(Cache c
             up = max(-90, min(100, up));
             const float mul = pow2(up);
             f = fmaxf(a.scale * 1.4426950408889634f * pow2(-up), 1.17549435e-38f);
+            // each of the two threads stores every other chunk
 #pragma unroll 4
-            for (int i = 0; i < D / 8; ++i) {
+            for (int i = half; i < D / 8; i += 2) {
                 const uint4 x = real ? __ldg(reinterpret_cast<const uint4*>(src) + i) : make_uint4(0, 0, 0, 0);
                 const float2 e01 = to_f32x2<BF16>(x.x), e23 = to_f32x2<BF16>(x.y);
                 const float2 e45 = to_f32x2<BF16>(x.z), e67 = to_f32x2<BF16>(x.w);
@@ -462,27 +468,29 @@ __global__ void __launch_bounds__(Prompt<NG>::kThreads, 1) prompt_kernel(Cache c
             const uint32_t phase = WIDE ? static_cast<uint32_t>((j >> 1) & 1) : static_cast<uint32_t>(j & 1);
             ok = ok && wait_bar(bar(&bars->s_full[sb]), phase, abort) &&
                  wait_bar(bar(&bars->info[j % kInfo]), static_cast<uint32_t>((j / kInfo) & 1), abort);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
+            ok = __all_sync(0xffffffffu, ok);   // a warp that gives up says so to the one it shares rows with below
             fa::ptx::tc_fence_after_sync();
             const TileInfo info = bars->tile[j % kInfo];
-            const uint32_t tS = tmem + lane_off + sb * 128;
-            const int kv0 = (jb + j) * BN;
-            const bool edge = __any_sync(0xffffffffu, kv0 + BN - 1 > pos || kv0 < first || info.missing != 0);
+            // S of this half; P of 16 keys takes 8 columns from the buffer's start on
+            const uint32_t tS = tmem + lane_off + sb * 128 + half * HALF, tP = tmem + lane_off + sb * 128 + half * (HALF / 2);
+            const int kv0 = (jb + j) * BN + half * HALF;
+            const uint32_t missing = info.missing >> (half * (HALF / 16));
+            const bool edge = __any_sync(0xffffffffu, kv0 + HALF - 1 > pos || kv0 < first || missing != 0);
             const float zf = f * pow2(info.ek), ev = static_cast<float>(info.ev);
             auto mask = [&](uint32_t* s, int q) {   // columns 32 q .. 32 q + 31
                 // bit k: column k is seen
                 const int from = min(max(first - kv0 - 32 * q, 0), 32), to = min(max(pos - kv0 - 32 * q + 1, 0), 32);
                 uint32_t seen = (to == 32 ? 0xffffffffu : (1u << to) - 1u) & (from == 32 ? 0u : 0xffffffffu << from);
-                if ((info.missing >> (2 * q)) & 1u) seen &= 0xffff0000u;
-                if ((info.missing >> (2 * q)) & 2u) seen &= 0x0000ffffu;
+                if ((missing >> (2 * q)) & 1u) seen &= 0xffff0000u;
+                if ((missing >> (2 * q)) & 2u) seen &= 0x0000ffffu;
 #pragma unroll
                 for (int k = 0; k < 32; ++k)
                     if (!((seen >> k) & 1u)) s[k] = __float_as_uint(kNegInf);
             };
             float mx = kNegInf;
+            if (ok) {
 #pragma unroll
-            for (int q = 0; q < BN / 32; ++q) {
+              for (int q = 0; q < HALF / 32; ++q) {
                 uint32_t s[32];
                 fa::ptx::tmem_ld_32x32b_x32(tS + q * 32, s);
                 fa::ptx::tmem_ld_wait();
@@ -495,25 +503,41 @@ __global__ void __launch_bounds__(Prompt<NG>::kThreads, 1) prompt_kernel(Cache c
                     m1 = fa::ptx::fmax3(m1, __uint_as_float(s[k + 2]), __uint_as_float(s[k + 3]));
                 }
                 mx = fa::ptx::fmax3(mx, m0, m1);
+              }
             }
-            // the reference moves lazily, when p' would pass 2^kLazy
-            const float top = mx == kNegInf ? kNegInf : fmaf(mx, zf, ev);
+            // The reference moves lazily, when p' would pass 2^kLazy; both halves of
+            // a row move it alike.  The barrier also stands between the halves'
+            // reads of S and the stores of P over it.
+            float top = mx == kNegInf ? kNegInf : fmaf(mx, zf, ev);
+            if (!(top == top)) top = kNegInf;   // an infinite factor: the row is NaN anyway
             float alpha = 1.f;
-            const bool move = top > ref + kLazy;
-            if (move) {
-                alpha = fa::ptx::ex2_approx(ref - top);   // 0 on the first tile
-                ref = top;
+            bool move = top > ref + kLazy;
+            if (fa::ptx::named_barrier_or(pair_bar, 64, move || !ok)) {
+                constexpr uint32_t kGaveUp = 0x7fc0dead;   // (a maximum is never a NaN)
+                bars->half_max[t][half][r] = ok ? top : __uint_as_float(kGaveUp);
+                fa::ptx::named_barrier_sync(pair_bar, 64);
+                const float other = bars->half_max[t][half ^ 1][r];
+                fa::ptx::named_barrier_sync(pair_bar, 64);
+                if (!ok || __float_as_uint(other) == kGaveUp) {   // the same for all rows of both warps
+                    ok = false;
+                    break;
+                }
+                top = fmaxf(top, other);
+                move = top > ref + kLazy;
+                if (move) {
+                    alpha = fa::ptx::ex2_approx(ref - top);   // 0 on the first tile
+                    ref = top;
+                }
             }
             if (j > 0 && __any_sync(0xffffffffu, move)) {
                 // S of this tile came after P V of the one before (D <= 128); else that has a barrier of its own
                 if constexpr (WIDE) {
                     ok = wait_bar(bar(&bars->o_done), static_cast<uint32_t>((j - 1) & 1), abort);
                     ok = __all_sync(0xffffffffu, ok);
-                    if (!ok) break;
                     fa::ptx::tc_fence_after_sync();
                 }
 #pragma unroll 1
-                for (int q = 0; q < N / 32; ++q) {
+                for (int q = half; q < N / 32 && ok; q += 2) {
                     uint32_t o[32];
                     fa::ptx::tmem_ld_32x32b_x32(tO + q * 32, o);
                     fa::ptx::tmem_ld_wait();
@@ -525,17 +549,20 @@ __global__ void __launch_bounds__(Prompt<NG>::kThreads, 1) prompt_kernel(Cache c
             }
             if (info.nan != 0) {
                 for (int k = 0; k < BN; ++k) {
-                    const int key = kv0 + k;
+                    const int key = (jb + j) * BN + k;
                     if (key <= pos && key >= first) poison |= bars->nan_groups[j % kInfo][k];
                 }
             }
             const float off = ev + kPHead - (ref == kNegInf ? 0.f : ref);
             const float2 zf2 = make_float2(zf, zf), off2 = make_float2(off, off);
             float2 sum = make_float2(0.f, 0.f);
-            uint32_t left[BF16 ? 1 : BN / 2];
+            // P of a half lies over S of the first (of both: over columns 0 .. HALF - 1
+            // of the buffer, whose S the first half has to have read; what P's
+            // rounding left over the second's).  So all of S is read before any of P is stored.
+            uint32_t pk[HALF / 2], left[BF16 ? 1 : HALF / 2];
 #pragma unroll
-            for (int q = 0; q < BN / 32; ++q) {
-                uint32_t s[32], pk[16];
+            for (int q = 0; q < HALF / 32; ++q) {
+                uint32_t s[32];
                 fa::ptx::tmem_ld_32x32b_x32(tS + q * 32, s);
                 fa::ptx::tmem_ld_wait();
                 fa::ptx::reg_fence<32>(s);
@@ -546,18 +573,20 @@ __global__ void __launch_bounds__(Prompt<NG>::kThreads, 1) prompt_kernel(Cache c
                                                 zf2, off2);
                     const float2 p = make_float2(fa::ptx::ex2_approx(x.x), fa::ptx::ex2_approx(x.y));
                     sum = __fadd2_rn(sum, p);
-                    pk[k] = pack16<false>(p.x, p.y);
+                    pk[q * 16 + k] = pack16<false>(p.x, p.y);
                     if constexpr (!BF16) {
-                        const float2 got = to_f32x2<false>(pk[k]);
+                        const float2 got = to_f32x2<false>(pk[q * 16 + k]);
                         left[q * 16 + k] = pack16<false>(p.x - got.x, p.y - got.y);
                     }
                 }
-                // P lies over S: columns 16 q .. of what has been read
-                fa::ptx::tmem_st_32x32b_x16(tS + q * 16, pk);
             }
-            if constexpr (!BF16) {
+            fa::ptx::tc_fence_before_sync();
+            fa::ptx::named_barrier_sync(pair_bar, 64);
+            fa::ptx::tc_fence_after_sync();
 #pragma unroll
-                for (int q = 0; q < BN / 32; ++q) fa::ptx::tmem_st_32x32b_x16(tS + BN / 2 + q * 16, left + q * 16);
+            for (int q = 0; q < HALF / 32; ++q) {
+                fa::ptx::tmem_st_32x32b_x16(tP + q * 16, pk + q * 16);
+                if constexpr (!BF16) fa::ptx::tmem_st_32x32b_x16(tP + HALF + q * 16, left + q * 16);
             }
             l = l * alpha + (sum.x + sum.y) * pow2(-info.ev);
             fa::ptx::tmem_st_wait();
@@ -568,13 +597,17 @@ __global__ void __launch_bounds__(Prompt<NG>::kThreads, 1) prompt_kernel(Cache c
         ok = ok && (n_tiles == 0 || wait_bar(bar(&bars->o_last), 0, abort));
         ok = __all_sync(0xffffffffu, ok);
         fa::ptx::tc_fence_after_sync();
+        // the halves' sums
+        bars->half_max[t][half][r] = l;
+        fa::ptx::named_barrier_sync(pair_bar, 64);
+        l += bars->half_max[t][half ^ 1][r];
         const float m = ref == kNegInf ? kNegInf : ref - kPHead;
         const long long slot = (static_cast<long long>(y - plan.whole) * splits + split) * TILES + t;
-        if (ok && splits > 1 && real) a.part_ml[slot * kRowTile + r] = make_float2(m, n_tiles > 0 ? l : 0.f);
+        if (ok && splits > 1 && real && half == 0) a.part_ml[slot * kRowTile + r] = make_float2(m, n_tiles > 0 ? l : 0.f);
         const float inv = l == 0.f ? 0.f : 1.f / l;
         if (ok) {
 #pragma unroll 1
-            for (int q = 0; q < NG; ++q) {
+            for (int q = half; q < NG; q += 2) {
                 uint32_t o[32];
                 if (n_tiles > 0) {
                     fa::ptx::tmem_ld_32x32b_x32(tO + q * 32, o);
@@ -608,7 +641,7 @@ __global__ void __launch_bounds__(Prompt<NG>::kThreads, 1) prompt_kernel(Cache c
                     }
                 }
             }
-            if (splits == 1 && real && a.lse != nullptr)
+            if (splits == 1 && real && half == 0 && a.lse != nullptr)
                 a.lse[(c.cu != nullptr ? w.row0 : b * a.lse_batch) + h * a.lse_head + qi] =
                     l == 0.f ? kNegInf : (m + log2f(l)) * 0.6931471805599453f;
         }
