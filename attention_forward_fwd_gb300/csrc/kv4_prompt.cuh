@@ -7,10 +7,13 @@
 // unpacked K and V), and walks over tiles of BN keys:
 //   unpack warps   codes and scales -> fp16 K and V tiles in shared memory
 //   MMA warp       S_t = Q_t K^T, O_t += P_t V (fp32 in tensor memory)
-//   softmax warps  two threads a row (TMEM lane), each with half of the keys:
-//                  S -> P (fp16, over S), the running maximum, O's rescaling,
-//                  the row sum.  (One thread a row takes 3700 cycles a tile,
-//                  nearly twice what the two products of both row tiles take.)
+//   softmax warps  thread = row = TMEM lane: S -> P (fp16, over S), the
+//                  running maximum, O's rescaling, the row sum.  A row of S is
+//                  read once and kept in registers, which the unpack warps give
+//                  up.  (Read in pieces of 32, with 96 registers, or by two
+//                  threads a row, which have to agree on the maximum, the
+//                  softmax of a tile took 3000 to 4000 cycles, against 2048
+//                  that both row tiles' products need.)
 // D <= 128: two row tiles that take turns on the tensor pipe (S_A, S_B, then
 // P_A V, S_A of the next keys, P_B V, ...).  D > 128: one row tile, as two O
 // tiles do not fit, with two S buffers (S of the next keys runs beside the softmax).
@@ -49,14 +52,19 @@ struct Prompt {
     static constexpr int BN = kWide ? 64 : 128;
     static constexpr int kBoxes = (NG + 1) / 2;            // 64 columns each
     static constexpr int N = kBoxes * 64;                  // columns of O (past D: zeros)
-    static constexpr int kSoftWarps = 8 * TILES;
+    static constexpr int kSoftWarps = 4 * TILES;
     static constexpr int kUnpackWarps = kWide ? 8 : 4;
     static constexpr int kMmaWarp = kSoftWarps + kUnpackWarps;
     static constexpr int kThreads = (kMmaWarp + 1) * 32;
     static constexpr int kQBox = kRowTile * 128, kBox = BN * 128;   // bytes
     static constexpr int kQTile = kBoxes * kQBox, kTile = kBoxes * kBox;
     static constexpr int kOffK = TILES * kQTile, kOffV = kOffK + 2 * kTile, kOffBar = kOffV + 2 * kTile;
-    static constexpr int kSmem = kOffBar + 4096 + 1024;    // and room to align
+    static constexpr int kSmem = kOffBar + 2048 + 1024;    // and room to align
+    // Registers a thread (D <= 128): 13 warps start with 128 each; 8 x 152 + 4 x 80
+    // + 128 of the MMA warp is what they started with.
+    static constexpr int kLaunchRegs = 128, kSoftRegs = 152, kUnpackRegs = 80;
+    static_assert(kWide || kSoftWarps * kSoftRegs + kUnpackWarps * kUnpackRegs + kLaunchRegs <=
+                               (kThreads / 32) * kLaunchRegs, "register split");
     static constexpr uint32_t kO = 256;                    // TMEM: S at 0 and 128, O from here on
     static_assert(kO + TILES * N <= 512, "tensor memory");
     static_assert(kSmem <= 232448, "shared memory");
@@ -74,12 +82,11 @@ struct PromptBars {
     TileInfo tile[kInfo];
     uint32_t top[2][8];                  // of each unpack warp: largest scales, K below V
     uint32_t gone[2][8];
-    float half_max[2][2][128];           // [row tile][half of the keys][row]
     uint8_t nan_groups[kInfo][128];      // of each key of V
     uint32_t tmem;
     int abort;
 };
-static_assert(sizeof(PromptBars) <= 4096, "barriers");
+static_assert(sizeof(PromptBars) <= 2048, "barriers");
 
 // The items (row tiles of R rows, K/V heads, sequences) in the order of the
 // grid; those of whole waves have a CTA each, those behind them `splits`.
@@ -105,6 +112,13 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile
             }
         }
     }
+}
+
+// 32 lanes x 8 columns of tensor memory
+__device__ __forceinline__ void tmem_ld_x8(uint32_t at, uint32_t* r) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(at));
 }
 
 __device__ __forceinline__ float pow2(int e) {   // -126 <= e <= 127
@@ -166,14 +180,14 @@ __global__ void __launch_bounds__(Prompt<NG>::kThreads, 1) prompt_kernel(Cache c
     const int n_tiles = t_lo + static_cast<int>(static_cast<long long>(t_all) * (split + 1) / splits) - jb;
 
     if (threadIdx.x == 0) {
-        fa::ptx::mbar_init(bar(&bars->q_full), 2 * R);
+        fa::ptx::mbar_init(bar(&bars->q_full), R);
         for (int i = 0; i < 2; ++i) {
             fa::ptx::mbar_init(bar(&bars->k_full[i]), kUnpackWarps);
             fa::ptx::mbar_init(bar(&bars->k_empty[i]), 1);
             fa::ptx::mbar_init(bar(&bars->v_full[i]), kUnpackWarps);
             fa::ptx::mbar_init(bar(&bars->v_empty[i]), 1);
             fa::ptx::mbar_init(bar(&bars->s_full[i]), 1);
-            fa::ptx::mbar_init(bar(&bars->p_full[i]), 2 * kRowTile);
+            fa::ptx::mbar_init(bar(&bars->p_full[i]), kRowTile);
         }
         for (int i = 0; i < kInfo; ++i) fa::ptx::mbar_init(bar(&bars->info[i]), 1);
         fa::ptx::mbar_init(bar(&bars->o_done), 1);
@@ -281,6 +295,7 @@ __global__ void __launch_bounds__(Prompt<NG>::kThreads, 1) prompt_kernel(Cache c
         wait_warp(bar(&bars->drain), 0, false);
     } else if (warp >= L::kSoftWarps) {
         // ---------------------------------------------------------- unpack
+        if constexpr (!WIDE) fa::ptx::setmaxnreg_dec<L::kUnpackRegs>();
         constexpr int CU = BN * 4 / (kUnpackWarps * 32);   // of the 4 units (c = 0 .. 3) of a key
         const int u = static_cast<int>(threadIdx.x) - L::kSoftWarps * 32;
         const int key = u % BN, c0 = u / BN * CU;          // this thread's units: c0 .. c0 + CU - 1
@@ -413,10 +428,9 @@ __global__ void __launch_bounds__(Prompt<NG>::kThreads, 1) prompt_kernel(Cache c
         }
     } else {
         // --------------------------------------------------------- softmax
-        constexpr int HALF = BN / 2;
-        const int t = warp >> 3, half = (warp >> 2) & 1;              // row tile, half of its keys
+        if constexpr (!WIDE) fa::ptx::setmaxnreg_inc<L::kSoftRegs>();
+        const int t = warp >> 2;                                      // row tile
         const int r = static_cast<int>(threadIdx.x) & 127;            // row of the tile, TMEM lane
-        const uint32_t pair_bar = 4 + t * 4 + (warp & 3);             // this warp and the one with the other half
         const int row = t * kRowTile + r, rho = tile * R + row;
         const bool real = row < rows;
         const int qi = rho / a.G, h = head * a.G + rho - qi * a.G;
@@ -445,9 +459,8 @@ __global__ void __launch_bounds__(Prompt<NG>::kThreads, 1) prompt_kernel(Cache c
             up = max(-90, min(100, up));
             const float mul = pow2(up);
             f = fmaxf(a.scale * 1.4426950408889634f * pow2(-up), 1.17549435e-38f);
-            // each of the two threads stores every other chunk
 #pragma unroll 4
-            for (int i = half; i < D / 8; i += 2) {
+            for (int i = 0; i < D / 8; ++i) {
                 const uint4 x = real ? __ldg(reinterpret_cast<const uint4*>(src) + i) : make_uint4(0, 0, 0, 0);
                 const float2 e01 = to_f32x2<BF16>(x.x), e23 = to_f32x2<BF16>(x.y);
                 const float2 e45 = to_f32x2<BF16>(x.z), e67 = to_f32x2<BF16>(x.w);
@@ -468,14 +481,14 @@ __global__ void __launch_bounds__(Prompt<NG>::kThreads, 1) prompt_kernel(Cache c
             const uint32_t phase = WIDE ? static_cast<uint32_t>((j >> 1) & 1) : static_cast<uint32_t>(j & 1);
             ok = ok && wait_bar(bar(&bars->s_full[sb]), phase, abort) &&
                  wait_bar(bar(&bars->info[j % kInfo]), static_cast<uint32_t>((j / kInfo) & 1), abort);
-            ok = __all_sync(0xffffffffu, ok);   // a warp that gives up says so to the one it shares rows with below
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
             fa::ptx::tc_fence_after_sync();
             const TileInfo info = bars->tile[j % kInfo];
-            // S of this half; P of 16 keys takes 8 columns from the buffer's start on
-            const uint32_t tS = tmem + lane_off + sb * 128 + half * HALF, tP = tmem + lane_off + sb * 128 + half * (HALF / 2);
-            const int kv0 = (jb + j) * BN + half * HALF;
-            const uint32_t missing = info.missing >> (half * (HALF / 16));
-            const bool edge = __any_sync(0xffffffffu, kv0 + HALF - 1 > pos || kv0 < first || missing != 0);
+            const uint32_t tS = tmem + lane_off + sb * 128;   // P lies over S, 16 keys in 8 columns
+            const int kv0 = (jb + j) * BN;
+            const uint32_t missing = info.missing;
+            const bool edge = __any_sync(0xffffffffu, kv0 + BN - 1 > pos || kv0 < first || missing != 0);
             const float zf = f * pow2(info.ek), ev = static_cast<float>(info.ev);
             auto mask = [&](uint32_t* s, int q) {   // columns 32 q .. 32 q + 31
                 // bit k: column k is seen
@@ -487,64 +500,47 @@ __global__ void __launch_bounds__(Prompt<NG>::kThreads, 1) prompt_kernel(Cache c
                 for (int k = 0; k < 32; ++k)
                     if (!((seen >> k) & 1u)) s[k] = __float_as_uint(kNegInf);
             };
-            float mx = kNegInf;
-            if (ok) {
+            uint32_t sv[BN];
 #pragma unroll
-              for (int q = 0; q < HALF / 32; ++q) {
-                uint32_t s[32];
-                fa::ptx::tmem_ld_32x32b_x32(tS + q * 32, s);
-                fa::ptx::tmem_ld_wait();
-                fa::ptx::reg_fence<32>(s);
-                if (edge) mask(s, q);
-                float m0 = kNegInf, m1 = kNegInf;
+            for (int q = 0; q < BN / 32; ++q) fa::ptx::tmem_ld_32x32b_x32(tS + q * 32, sv + q * 32);
+            fa::ptx::tmem_ld_wait();
+            fa::ptx::reg_fence<BN>(sv);
+            if (edge) {
 #pragma unroll
-                for (int k = 0; k < 32; k += 4) {
-                    m0 = fa::ptx::fmax3(m0, __uint_as_float(s[k]), __uint_as_float(s[k + 1]));
-                    m1 = fa::ptx::fmax3(m1, __uint_as_float(s[k + 2]), __uint_as_float(s[k + 3]));
-                }
-                mx = fa::ptx::fmax3(mx, m0, m1);
-              }
+                for (int q = 0; q < BN / 32; ++q) mask(sv + q * 32, q);
             }
-            // The reference moves lazily, when p' would pass 2^kLazy; both halves of
-            // a row move it alike.  The barrier also stands between the halves'
-            // reads of S and the stores of P over it.
-            float top = mx == kNegInf ? kNegInf : fmaf(mx, zf, ev);
-            if (!(top == top)) top = kNegInf;   // an infinite factor: the row is NaN anyway
+            float mx[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
+#pragma unroll
+            for (int k = 0; k < BN; k += 8)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    mx[i] = fa::ptx::fmax3(mx[i], __uint_as_float(sv[k + 2 * i]), __uint_as_float(sv[k + 2 * i + 1]));
+            mx[0] = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+            // the reference moves lazily, when p' would pass 2^kLazy
+            const float top = mx[0] == kNegInf ? kNegInf : fmaf(mx[0], zf, ev);
             float alpha = 1.f;
-            bool move = top > ref + kLazy;
-            if (fa::ptx::named_barrier_or(pair_bar, 64, move || !ok)) {
-                constexpr uint32_t kGaveUp = 0x7fc0dead;   // (a maximum is never a NaN)
-                bars->half_max[t][half][r] = ok ? top : __uint_as_float(kGaveUp);
-                fa::ptx::named_barrier_sync(pair_bar, 64);
-                const float other = bars->half_max[t][half ^ 1][r];
-                fa::ptx::named_barrier_sync(pair_bar, 64);
-                if (!ok || __float_as_uint(other) == kGaveUp) {   // the same for all rows of both warps
-                    ok = false;
-                    break;
-                }
-                top = fmaxf(top, other);
-                move = top > ref + kLazy;
-                if (move) {
-                    alpha = fa::ptx::ex2_approx(ref - top);   // 0 on the first tile
-                    ref = top;
-                }
+            const bool move = top > ref + kLazy;
+            if (move) {
+                alpha = fa::ptx::ex2_approx(ref - top);   // 0 on the first tile
+                ref = top;
             }
             if (j > 0 && __any_sync(0xffffffffu, move)) {
                 // S of this tile came after P V of the one before (D <= 128); else that has a barrier of its own
                 if constexpr (WIDE) {
                     ok = wait_bar(bar(&bars->o_done), static_cast<uint32_t>((j - 1) & 1), abort);
                     ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
                     fa::ptx::tc_fence_after_sync();
                 }
 #pragma unroll 1
-                for (int q = half; q < N / 32 && ok; q += 2) {
-                    uint32_t o[32];
-                    fa::ptx::tmem_ld_32x32b_x32(tO + q * 32, o);
+                for (int q = 0; q < N / 8; ++q) {   // few registers: the row of S is held
+                    uint32_t o[8];
+                    tmem_ld_x8(tO + q * 8, o);
                     fa::ptx::tmem_ld_wait();
-                    fa::ptx::reg_fence<32>(o);
+                    fa::ptx::reg_fence<8>(o);
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
-                    fa::ptx::tmem_st_32x32b_x32(tO + q * 32, o);
+                    for (int k = 0; k < 8; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+                    fa::ptx::tmem_st_32x32b_x8(tO + q * 8, o);
                 }
             }
             if (info.nan != 0) {
@@ -556,37 +552,23 @@ __global__ void __launch_bounds__(Prompt<NG>::kThreads, 1) prompt_kernel(Cache c
             const float off = ev + kPHead - (ref == kNegInf ? 0.f : ref);
             const float2 zf2 = make_float2(zf, zf), off2 = make_float2(off, off);
             float2 sum = make_float2(0.f, 0.f);
-            // P of a half lies over S of the first (of both: over columns 0 .. HALF - 1
-            // of the buffer, whose S the first half has to have read; what P's
-            // rounding left over the second's).  So all of S is read before any of P is stored.
-            uint32_t pk[HALF / 2], left[BF16 ? 1 : HALF / 2];
 #pragma unroll
-            for (int q = 0; q < HALF / 32; ++q) {
-                uint32_t s[32];
-                fa::ptx::tmem_ld_32x32b_x32(tS + q * 32, s);
-                fa::ptx::tmem_ld_wait();
-                fa::ptx::reg_fence<32>(s);
-                if (edge) mask(s, q);
+            for (int q = 0; q < BN / 16; ++q) {
+                uint32_t pk[8], left[8];
 #pragma unroll
-                for (int k = 0; k < 16; ++k) {
-                    const float2 x = __ffma2_rn(make_float2(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1])),
-                                                zf2, off2);
+                for (int k = 0; k < 8; ++k) {
+                    const float2 x = __ffma2_rn(make_float2(__uint_as_float(sv[q * 16 + 2 * k]),
+                                                            __uint_as_float(sv[q * 16 + 2 * k + 1])), zf2, off2);
                     const float2 p = make_float2(fa::ptx::ex2_approx(x.x), fa::ptx::ex2_approx(x.y));
                     sum = __fadd2_rn(sum, p);
-                    pk[q * 16 + k] = pack16<false>(p.x, p.y);
+                    pk[k] = pack16<false>(p.x, p.y);
                     if constexpr (!BF16) {
-                        const float2 got = to_f32x2<false>(pk[q * 16 + k]);
-                        left[q * 16 + k] = pack16<false>(p.x - got.x, p.y - got.y);
+                        const float2 got = to_f32x2<false>(pk[k]);
+                        left[k] = pack16<false>(p.x - got.x, p.y - got.y);
                     }
                 }
-            }
-            fa::ptx::tc_fence_before_sync();
-            fa::ptx::named_barrier_sync(pair_bar, 64);
-            fa::ptx::tc_fence_after_sync();
-#pragma unroll
-            for (int q = 0; q < HALF / 32; ++q) {
-                fa::ptx::tmem_st_32x32b_x16(tP + q * 16, pk + q * 16);
-                if constexpr (!BF16) fa::ptx::tmem_st_32x32b_x16(tP + HALF + q * 16, left + q * 16);
+                fa::ptx::tmem_st_32x32b_x8(tS + q * 8, pk);
+                if constexpr (!BF16) fa::ptx::tmem_st_32x32b_x8(tS + BN / 2 + q * 8, left);
             }
             l = l * alpha + (sum.x + sum.y) * pow2(-info.ev);
             fa::ptx::tmem_st_wait();
@@ -597,17 +579,13 @@ __global__ void __launch_bounds__(Prompt<NG>::kThreads, 1) prompt_kernel(Cache c
         ok = ok && (n_tiles == 0 || wait_bar(bar(&bars->o_last), 0, abort));
         ok = __all_sync(0xffffffffu, ok);
         fa::ptx::tc_fence_after_sync();
-        // the halves' sums
-        bars->half_max[t][half][r] = l;
-        fa::ptx::named_barrier_sync(pair_bar, 64);
-        l += bars->half_max[t][half ^ 1][r];
         const float m = ref == kNegInf ? kNegInf : ref - kPHead;
         const long long slot = (static_cast<long long>(y - plan.whole) * splits + split) * TILES + t;
-        if (ok && splits > 1 && real && half == 0) a.part_ml[slot * kRowTile + r] = make_float2(m, n_tiles > 0 ? l : 0.f);
+        if (ok && splits > 1 && real) a.part_ml[slot * kRowTile + r] = make_float2(m, n_tiles > 0 ? l : 0.f);
         const float inv = l == 0.f ? 0.f : 1.f / l;
         if (ok) {
 #pragma unroll 1
-            for (int q = half; q < NG; q += 2) {
+            for (int q = 0; q < NG; ++q) {
                 uint32_t o[32];
                 if (n_tiles > 0) {
                     fa::ptx::tmem_ld_32x32b_x32(tO + q * 32, o);
@@ -641,7 +619,7 @@ __global__ void __launch_bounds__(Prompt<NG>::kThreads, 1) prompt_kernel(Cache c
                     }
                 }
             }
-            if (splits == 1 && real && half == 0 && a.lse != nullptr)
+            if (splits == 1 && real && a.lse != nullptr)
                 a.lse[(c.cu != nullptr ? w.row0 : b * a.lse_batch) + h * a.lse_head + qi] =
                     l == 0.f ? kNegInf : (m + log2f(l)) * 0.6931471805599453f;
         }
