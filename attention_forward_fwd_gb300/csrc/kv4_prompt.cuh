@@ -8,12 +8,10 @@
 //   unpack warps   codes and scales -> fp16 K and V tiles in shared memory
 //   MMA warp       S_t = Q_t K^T, O_t += P_t V (fp32 in tensor memory)
 //   softmax warps  thread = row = TMEM lane: S -> P (fp16, over S), the
-//                  running maximum, O's rescaling, the row sum.  A row of S is
-//                  read once and kept in registers, which the unpack warps give
-//                  up.  (Read in pieces of 32, with 96 registers, or by two
-//                  threads a row, which have to agree on the maximum, the
-//                  softmax of a tile took 3000 to 4000 cycles, against 2048
-//                  that both row tiles' products need.)
+//                  running maximum, O's rescaling, the row sum.  S is read in
+//                  quarters, the next one while one is worked on.  The last
+//                  two stay in registers from the maximum to the exponentials, and P
+//                  goes over the second half of S, so that the first two can be read again.
 // D <= 128: two row tiles that take turns on the tensor pipe (S_A, S_B, then
 // P_A V, S_A of the next keys, P_B V, ...).  D > 128: one row tile, as two O
 // tiles do not fit, with two S buffers (S of the next keys runs beside the softmax).
@@ -30,6 +28,11 @@
 // Elements 8 i .. 8 i + 7 of a row lie in the order 0 4 1 5 2 6 3 7 in all three
 // tiles: codes come out of their words in pairs (j, 4 + j), and a contraction
 // does not care; O's columns are put back in the epilogue.
+//
+// The code of the three roles has to stay small: with every loop unrolled and the
+// masks inline the warps waited for instructions nearly twice as long as they
+// ran them.  Tiles that need a mask have it written over S first, in a loop of its
+// own, K and V share the unpacking code, both row tiles the issuing code.
 //
 // What bounds it: softmax and tensor pipe, as in the plain forward, and beside
 // them the unpacking, 32,768 values a tile of 128 keys at D = 128 for about 2.2
@@ -60,11 +63,6 @@ struct Prompt {
     static constexpr int kQTile = kBoxes * kQBox, kTile = kBoxes * kBox;
     static constexpr int kOffK = TILES * kQTile, kOffV = kOffK + 2 * kTile, kOffBar = kOffV + 2 * kTile;
     static constexpr int kSmem = kOffBar + 2048 + 1024;    // and room to align
-    // Registers a thread (D <= 128): 13 warps start with 128 each; 8 x 152 + 4 x 80
-    // + 128 of the MMA warp is what they started with.
-    static constexpr int kLaunchRegs = 128, kSoftRegs = 152, kUnpackRegs = 80;
-    static_assert(kWide || kSoftWarps * kSoftRegs + kUnpackWarps * kUnpackRegs + kLaunchRegs <=
-                               (kThreads / 32) * kLaunchRegs, "register split");
     static constexpr uint32_t kO = 256;                    // TMEM: S at 0 and 128, O from here on
     static_assert(kO + TILES * N <= 512, "tensor memory");
     static_assert(kSmem <= 232448, "shared memory");
@@ -77,8 +75,8 @@ struct TileInfo {
 };
 
 struct PromptBars {
-    uint64_t q_full, k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_done, o_last, info[kInfo],
-        drain;
+    uint64_t q_full, full[2][2], empty[2][2];   // [K or V][slot]
+    uint64_t s_full[2], p_full[2], o_done, o_last, info[kInfo], drain;
     TileInfo tile[kInfo];
     uint32_t top[2][8];                  // of each unpack warp: largest scales, K below V
     uint32_t gone[2][8];
@@ -119,6 +117,20 @@ __device__ __forceinline__ void tmem_ld_x8(uint32_t at, uint32_t* r) {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
                  : "r"(at));
+}
+
+__device__ __forceinline__ void tmem_ld_x16(uint32_t at, uint32_t* r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+        "[%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(at));
+}
+template <int N>
+__device__ __forceinline__ void store_p(uint32_t at, const uint32_t* p) {
+    if constexpr (N == 16) fa::ptx::tmem_st_32x32b_x16(at, p);
+    else fa::ptx::tmem_st_32x32b_x8(at, p);
 }
 
 __device__ __forceinline__ float pow2(int e) {   // -126 <= e <= 127
@@ -182,10 +194,10 @@ __global__ void __launch_bounds__(Prompt<NG>::kThreads, 1) prompt_kernel(Cache c
     if (threadIdx.x == 0) {
         fa::ptx::mbar_init(bar(&bars->q_full), R);
         for (int i = 0; i < 2; ++i) {
-            fa::ptx::mbar_init(bar(&bars->k_full[i]), kUnpackWarps);
-            fa::ptx::mbar_init(bar(&bars->k_empty[i]), 1);
-            fa::ptx::mbar_init(bar(&bars->v_full[i]), kUnpackWarps);
-            fa::ptx::mbar_init(bar(&bars->v_empty[i]), 1);
+            for (int x = 0; x < 2; ++x) {
+                fa::ptx::mbar_init(bar(&bars->full[x][i]), kUnpackWarps);
+                fa::ptx::mbar_init(bar(&bars->empty[x][i]), 1);
+            }
             fa::ptx::mbar_init(bar(&bars->s_full[i]), 1);
             fa::ptx::mbar_init(bar(&bars->p_full[i]), kRowTile);
         }
@@ -245,31 +257,29 @@ __global__ void __launch_bounds__(Prompt<NG>::kThreads, 1) prompt_kernel(Cache c
             for (int part = 0; part < (BF16 ? 1 : 2); ++part)     // and what P's rounding left
 #pragma unroll
                 for (int x = 0; x < BN / 16; x += 4)
-                    fa::ptx::mma_ts_x4_lo(tmem + L::kO + t * N, tmem + s * 128 + part * (BN / 2) + x * 8, v + x * 128, hi, 8u,
+                    fa::ptx::mma_ts_x4_lo(tmem + L::kO + t * N, tmem + s * 128 + (1 - part) * (BN / 2) + x * 8, v + x * 128, hi, 8u,
                                           128u, kIdescO, (j > 0 || x > 0 || part > 0) ? 1u : 0u);
         };
         if constexpr (!WIDE) {
-            if (ok && n_tiles > 0 && (ok = wait_warp(bar(&bars->k_full[0]), 0))) {
-                issue_s(0, 0, 0);
-                issue_s(0, 1, 1);
-                fa::ptx::tc_commit_warp(bar(&bars->k_empty[0]));
-            }
-            for (int j = 0; j < n_tiles && ok; ++j) {
-#pragma unroll
+            // j = -1: S of the first tile alone
+            for (int j = -1; j < n_tiles && ok; ++j) {
+#pragma unroll 1
                 for (int t = 0; t < TILES; ++t) {
+                  if (j >= 0) {
                     if (!(ok = wait_warp(bar(&bars->p_full[t]), static_cast<uint32_t>(j & 1)))) break;
-                    if (t == 0 && !(ok = wait_warp(bar(&bars->v_full[j & 1]), static_cast<uint32_t>((j >> 1) & 1)))) break;
+                    if (t == 0 && !(ok = wait_warp(bar(&bars->full[1][j & 1]), static_cast<uint32_t>((j >> 1) & 1)))) break;
                     issue_o(j, t, t);
                     if (t == TILES - 1) {
-                        fa::ptx::tc_commit_warp(bar(&bars->v_empty[j & 1]));
+                        fa::ptx::tc_commit_warp(bar(&bars->empty[1][j & 1]));
                         if (j + 1 == n_tiles) fa::ptx::tc_commit_warp(bar(&bars->o_last));
                     }
+                  }
                     if (j + 1 < n_tiles) {
                         if (t == 0 &&
-                            !(ok = wait_warp(bar(&bars->k_full[(j + 1) & 1]), static_cast<uint32_t>(((j + 1) >> 1) & 1))))
+                            !(ok = wait_warp(bar(&bars->full[0][(j + 1) & 1]), static_cast<uint32_t>(((j + 1) >> 1) & 1))))
                             break;
                         issue_s(j + 1, t, t);
-                        if (t == TILES - 1) fa::ptx::tc_commit_warp(bar(&bars->k_empty[(j + 1) & 1]));
+                        if (t == TILES - 1) fa::ptx::tc_commit_warp(bar(&bars->empty[0][(j + 1) & 1]));
                     }
                 }
             }
@@ -277,15 +287,15 @@ __global__ void __launch_bounds__(Prompt<NG>::kThreads, 1) prompt_kernel(Cache c
             for (int j = -1; j < n_tiles && ok; ++j) {
                 if (j + 1 < n_tiles) {
                     const int i = j + 1;
-                    if (!(ok = wait_warp(bar(&bars->k_full[i & 1]), static_cast<uint32_t>((i >> 1) & 1)))) break;
+                    if (!(ok = wait_warp(bar(&bars->full[0][i & 1]), static_cast<uint32_t>((i >> 1) & 1)))) break;
                     issue_s(i, 0, i & 1);
-                    fa::ptx::tc_commit_warp(bar(&bars->k_empty[i & 1]));
+                    fa::ptx::tc_commit_warp(bar(&bars->empty[0][i & 1]));
                 }
                 if (j < 0) continue;
                 if (!(ok = wait_warp(bar(&bars->p_full[j & 1]), static_cast<uint32_t>((j >> 1) & 1)))) break;
-                if (!(ok = wait_warp(bar(&bars->v_full[j & 1]), static_cast<uint32_t>((j >> 1) & 1)))) break;
+                if (!(ok = wait_warp(bar(&bars->full[1][j & 1]), static_cast<uint32_t>((j >> 1) & 1)))) break;
                 issue_o(j, 0, j & 1);
-                fa::ptx::tc_commit_warp(bar(&bars->v_empty[j & 1]));
+                fa::ptx::tc_commit_warp(bar(&bars->empty[1][j & 1]));
                 fa::ptx::tc_commit_warp(bar(&bars->o_done));
                 if (j + 1 == n_tiles) fa::ptx::tc_commit_warp(bar(&bars->o_last));
             }
@@ -295,7 +305,6 @@ __global__ void __launch_bounds__(Prompt<NG>::kThreads, 1) prompt_kernel(Cache c
         wait_warp(bar(&bars->drain), 0, false);
     } else if (warp >= L::kSoftWarps) {
         // ---------------------------------------------------------- unpack
-        if constexpr (!WIDE) fa::ptx::setmaxnreg_dec<L::kUnpackRegs>();
         constexpr int CU = BN * 4 / (kUnpackWarps * 32);   // of the 4 units (c = 0 .. 3) of a key
         const int u = static_cast<int>(threadIdx.x) - L::kSoftWarps * 32;
         const int key = u % BN, c0 = u / BN * CU;          // this thread's units: c0 .. c0 + CU - 1
@@ -310,12 +319,11 @@ __global__ void __launch_bounds__(Prompt<NG>::kThreads, 1) prompt_kernel(Cache c
             }
         }
         const int* table = c.table + static_cast<long long>(b) * c.max_pages;
-        // The rows of tile j + 1 are asked for as those of tile j have been
-        // unpacked (K's latency runs beside V's unpacking and the other way
-        // round), their scales as tile j begins, their page a tile before that.
-        Words<2 * NG> kr[CU], vr[CU];
+        // K's rows of a tile, V's, K's of the next one, ...: each asked for as the
+        // ones before them are unpacked; the scales a tile ahead, the page two.
+        Words<2 * NG> raw[CU];
         Words<NG> ks, vs, ks2, vs2;
-        long long row2 = -1;        // row of the next tile's key in the cache; -1: none
+        long long row = -1, row2 = -1;   // of the key in the cache, this tile and the next; -1: none
         bool gone = false, gone2 = false;
         int next = jb * BN + key;   // position that `pg`, `off` and `page` stand for
         int pg = next / c.P, off = next - pg * c.P, page = -1, tile_at = 0;
@@ -353,13 +361,13 @@ __global__ void __launch_bounds__(Prompt<NG>::kThreads, 1) prompt_kernel(Cache c
         };
         look_up();
         advance();
-        load_rows(kr, row2);
-        load_rows(vr, row2 < 0 ? -1 : row2 + k_to_v);
+        load_rows(raw, row2);
         bool ok = true;
         for (int j = 0; j < n_tiles; ++j) {
             ks = ks2;
             vs = vs2;
             gone = gone2;
+            row = row2;
             advance();
             // ---- the tile's largest finite scales, NaNs and holes
             uint32_t kt = 0, vt = 0, nan_groups = 0;
@@ -403,32 +411,28 @@ __global__ void __launch_bounds__(Prompt<NG>::kThreads, 1) prompt_kernel(Cache c
                 fa::ptx::mbar_arrive(bar(&bars->info[j % kInfo]));
             }
             // ---- K, then V, each once its slot is free
-            if (j >= 2)
-                ok = ok && wait_warp(bar(&bars->k_empty[j & 1]), static_cast<uint32_t>(((j >> 1) - 1) & 1));
-            ok = __all_sync(0xffffffffu, ok);
-            if (ok) {
-                uint8_t* kt_at = smem + L::kOffK + (j & 1) * L::kTile;
+#pragma unroll 1
+            for (int x = 0; x < 2; ++x) {
+                if (j >= 2)
+                    ok = ok && wait_warp(bar(&bars->empty[x][j & 1]), static_cast<uint32_t>(((j >> 1) - 1) & 1));
+                Words<2 * NG> ahead[CU];
+                load_rows(ahead, x == 0 ? (row < 0 ? -1 : row + k_to_v) : row2);
+                if (ok) {
+                    uint8_t* to = smem + (x == 0 ? L::kOffK : L::kOffV) + (j & 1) * L::kTile;
+                    const float down = pow2(x == 0 ? -ek : -ev);
 #pragma unroll
-                for (int i = 0; i < CU; ++i) unpack_unit<NG, L::kBox>(kr[i], ks, pow2(-ek), c0 + i, key, kt_at);
-                fa::ptx::fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) fa::ptx::mbar_arrive(bar(&bars->k_full[j & 1]));
-                load_rows(kr, row2);
-                if (j >= 2) ok = wait_warp(bar(&bars->v_empty[j & 1]), static_cast<uint32_t>(((j >> 1) - 1) & 1));
-            }
-            if (ok) {
-                uint8_t* vt_at = smem + L::kOffV + (j & 1) * L::kTile;
+                    for (int i = 0; i < CU; ++i) unpack_unit<NG, L::kBox>(raw[i], ks, down, c0 + i, key, to);
+                    fa::ptx::fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) fa::ptx::mbar_arrive(bar(&bars->full[x][j & 1]));
+                }
+                ks = vs;
 #pragma unroll
-                for (int i = 0; i < CU; ++i) unpack_unit<NG, L::kBox>(vr[i], vs, pow2(-ev), c0 + i, key, vt_at);
-                fa::ptx::fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) fa::ptx::mbar_arrive(bar(&bars->v_full[j & 1]));
-                load_rows(vr, row2 < 0 ? -1 : row2 + k_to_v);
+                for (int i = 0; i < CU; ++i) raw[i] = ahead[i];
             }
         }
     } else {
         // --------------------------------------------------------- softmax
-        if constexpr (!WIDE) fa::ptx::setmaxnreg_inc<L::kSoftRegs>();
         const int t = warp >> 2;                                      // row tile
         const int r = static_cast<int>(threadIdx.x) & 127;            // row of the tile, TMEM lane
         const int row = t * kRowTile + r, rho = tile * R + row;
@@ -485,36 +489,52 @@ __global__ void __launch_bounds__(Prompt<NG>::kThreads, 1) prompt_kernel(Cache c
             if (!ok) break;
             fa::ptx::tc_fence_after_sync();
             const TileInfo info = bars->tile[j % kInfo];
-            const uint32_t tS = tmem + lane_off + sb * 128;   // P lies over S, 16 keys in 8 columns
+            const uint32_t tS = tmem + lane_off + sb * 128;
             const int kv0 = (jb + j) * BN;
             const uint32_t missing = info.missing;
             const bool edge = __any_sync(0xffffffffu, kv0 + BN - 1 > pos || kv0 < first || missing != 0);
             const float zf = f * pow2(info.ek), ev = static_cast<float>(info.ev);
-            auto mask = [&](uint32_t* s, int q) {   // columns 32 q .. 32 q + 31
-                // bit k: column k is seen
-                const int from = min(max(first - kv0 - 32 * q, 0), 32), to = min(max(pos - kv0 - 32 * q + 1, 0), 32);
-                uint32_t seen = (to == 32 ? 0xffffffffu : (1u << to) - 1u) & (from == 32 ? 0u : 0xffffffffu << from);
-                if ((missing >> (2 * q)) & 1u) seen &= 0xffff0000u;
-                if ((missing >> (2 * q)) & 2u) seen &= 0x0000ffffu;
-#pragma unroll
-                for (int k = 0; k < 32; ++k)
-                    if (!((seen >> k) & 1u)) s[k] = __float_as_uint(kNegInf);
+            constexpr int QK = BN / 4;   // keys of a quarter
+            auto read = [&](uint32_t* s, int q) {
+                if constexpr (QK == 32) fa::ptx::tmem_ld_32x32b_x32(tS + q * QK, s);
+                else tmem_ld_x16(tS + q * QK, s);
             };
-            uint32_t sv[BN];
-#pragma unroll
-            for (int q = 0; q < BN / 32; ++q) fa::ptx::tmem_ld_32x32b_x32(tS + q * 32, sv + q * 32);
-            fa::ptx::tmem_ld_wait();
-            fa::ptx::reg_fence<BN>(sv);
+            auto arrived = [&](uint32_t* s, int q) {
+                fa::ptx::tmem_ld_wait();
+                fa::ptx::reg_fence<QK>(s);
+            };
             if (edge) {
+                // masked scores become -inf where they are
+#pragma unroll 1
+                for (int q = 0; q < BN / 8; ++q) {
+                    uint32_t s[8];
+                    tmem_ld_x8(tS + q * 8, s);
+                    fa::ptx::tmem_ld_wait();
+                    fa::ptx::reg_fence<8>(s);
+                    const bool hole = (missing >> (q / 2)) & 1u;
 #pragma unroll
-                for (int q = 0; q < BN / 32; ++q) mask(sv + q * 32, q);
+                    for (int k = 0; k < 8; ++k) {
+                        const int key = kv0 + q * 8 + k;
+                        if (hole || key > pos || key < first) s[k] = __float_as_uint(kNegInf);
+                    }
+                    fa::ptx::tmem_st_32x32b_x8(tS + q * 8, s);
+                }
+                fa::ptx::tmem_st_wait();
             }
+            uint32_t buf[2][QK];
             float mx[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
+            read(buf[0], 0);
 #pragma unroll
-            for (int k = 0; k < BN; k += 8)
+            for (int q = 0; q < 4; ++q) {
+                arrived(buf[q & 1], q);
+                if (q < 3) read(buf[(q + 1) & 1], q + 1);
+                uint32_t* s = buf[q & 1];
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    mx[i] = fa::ptx::fmax3(mx[i], __uint_as_float(sv[k + 2 * i]), __uint_as_float(sv[k + 2 * i + 1]));
+                for (int k = 0; k < QK; k += 8)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        mx[i] = fa::ptx::fmax3(mx[i], __uint_as_float(s[k + 2 * i]), __uint_as_float(s[k + 2 * i + 1]));
+            }
             mx[0] = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
             // the reference moves lazily, when p' would pass 2^kLazy
             const float top = mx[0] == kNegInf ? kNegInf : fmaf(mx[0], zf, ev);
@@ -551,26 +571,41 @@ __global__ void __launch_bounds__(Prompt<NG>::kThreads, 1) prompt_kernel(Cache c
             }
             const float off = ev + kPHead - (ref == kNegInf ? 0.f : ref);
             const float2 zf2 = make_float2(zf, zf), off2 = make_float2(off, off);
-            float2 sum = make_float2(0.f, 0.f);
+            float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+            // the quarters 2, 3, 0, 1: P of q in columns BN / 2 + q QK / 2 on, what its
+            // rounding left in q QK / 2 on, which has to wait until S has been read there
+            uint32_t left[BF16 ? 1 : 2][QK / 2];
 #pragma unroll
-            for (int q = 0; q < BN / 16; ++q) {
-                uint32_t pk[8], left[8];
+            for (int i = 0; i < 4; ++i) {
+                const int q = (i + 2) & 3;
+                uint32_t* s = buf[i & 1];
+                if (i >= 2) {
+                    arrived(s, q);
+                    if constexpr (!BF16)
+                        if (i == 2) {   // the wait was for quarter 1 as well
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const float2 x = __ffma2_rn(make_float2(__uint_as_float(sv[q * 16 + 2 * k]),
-                                                            __uint_as_float(sv[q * 16 + 2 * k + 1])), zf2, off2);
+                            for (int h = 0; h < 2; ++h) store_p<QK / 2>(tS + (2 + h) * (QK / 2), left[h]);
+                        }
+                }
+                uint32_t pk[QK / 2];
+#pragma unroll
+                for (int k = 0; k < QK / 2; ++k) {
+                    const float2 x = __ffma2_rn(make_float2(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1])),
+                                                zf2, off2);
                     const float2 p = make_float2(fa::ptx::ex2_approx(x.x), fa::ptx::ex2_approx(x.y));
-                    sum = __fadd2_rn(sum, p);
+                    sum[k & 1] = __fadd2_rn(sum[k & 1], p);
                     pk[k] = pack16<false>(p.x, p.y);
                     if constexpr (!BF16) {
                         const float2 got = to_f32x2<false>(pk[k]);
-                        left[k] = pack16<false>(p.x - got.x, p.y - got.y);
+                        left[i & 1][k] = pack16<false>(p.x - got.x, p.y - got.y);
                     }
                 }
-                fa::ptx::tmem_st_32x32b_x8(tS + q * 8, pk);
-                if constexpr (!BF16) fa::ptx::tmem_st_32x32b_x8(tS + BN / 2 + q * 8, left);
+                if (i < 2) read(s, i);   // quarter 0 or 1 again
+                store_p<QK / 2>(tS + BN / 2 + q * (QK / 2), pk);
+                if constexpr (!BF16)
+                    if (i >= 2) store_p<QK / 2>(tS + q * (QK / 2), left[i & 1]);
             }
-            l = l * alpha + (sum.x + sum.y) * pow2(-info.ev);
+            l = l * alpha + ((sum[0].x + sum[0].y) + (sum[1].x + sum[1].y)) * pow2(-info.ev);
             fa::ptx::tmem_st_wait();
             fa::ptx::tc_fence_before_sync();
             fa::ptx::mbar_arrive(bar(&bars->p_full[sb]));
