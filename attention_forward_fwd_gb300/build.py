@@ -77,6 +77,9 @@ def needs_build(debug: bool = False) -> bool:
 # smaller launch budget would leave the increasing warpgroups waiting for
 # registers that never come.
 KERNEL_LAUNCH_REGS = {1: 168, 2: 96}
+# The same for prompt_kernel of the quantised cache, for heads of at most 4
+# groups of 32 (kv4_prompt.cuh, Prompt::kLaunchRegs); wider ones do not re-split.
+PROMPT_LAUNCH_REGS, PROMPT_RESPLIT_GROUPS = 96, 4
 
 
 def _expected_regs(mangled: str) -> int:
@@ -87,8 +90,8 @@ def _expected_regs(mangled: str) -> int:
 
 
 def check_launch_registers(ptxas_log: str) -> None:
-    """Raise unless every fa_fwd_kernel instantiation launches with the
-    register count its setmaxnreg split assumes."""
+    """Raise unless every fa_fwd_kernel and prompt_kernel instantiation
+    launches with the register count its setmaxnreg split assumes."""
     current = None
     seen = 0
     for line in ptxas_log.splitlines():
@@ -98,9 +101,14 @@ def check_launch_registers(ptxas_log: str) -> None:
             continue
         m = re.search(r"Used (\d+) registers", line)
         if m and current is not None:
+            prompt = re.search(r"13prompt_kernelILi(\d+)E", current)
+            want = None
             if "fa_fwd_kernel" in current:
                 seen += 1
                 want = _expected_regs(current)
+            elif prompt and int(prompt.group(1)) <= PROMPT_RESPLIT_GROUPS:
+                want = PROMPT_LAUNCH_REGS
+            if want is not None:
                 if int(m.group(1)) != want:
                     raise RuntimeError(
                         f"{current} uses {m.group(1)} registers per thread, not "

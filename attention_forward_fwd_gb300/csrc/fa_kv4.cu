@@ -170,11 +170,11 @@ int prompt(const kv4::Cache& c, kv4::Attend a, void* ws, size_t ws_bytes, Decode
     if (!resident(res, kernel, L::kThreads, L::kSmem, &sms, &ctas)) return FA_ERR_CUDA;
     kv4::PromptPlan plan;
     const long long tiles = (static_cast<long long>(c.S) * a.G + R - 1) / R, items = tiles * c.Hkv * c.B;
-    const long long keys = (static_cast<long long>(c.max_pages) * c.P + L::BN - 1) / L::BN;
+    const long long keys = (static_cast<long long>(c.max_pages) * c.P + L::kGroupKeys - 1) / L::kGroupKeys;   // groups
     plan.tiles_most = static_cast<int>(tiles);
     // The items behind the last whole wave of CTAs share their keys out so that
-    // the SMs end together: s CTAs an item, each with its share of the key
-    // tiles and about three tiles' time to start and end, and a second launch.
+    // the SMs end together: s CTAs an item, each with its share of the groups of
+    // keys (4 at least) and about three groups' time to start and end, and a second launch.
     const long long whole = items / sms * sms, rest = items - whole;
     long long best = rest > 0 ? keys + 3 : 0;
     plan.whole = static_cast<int>(std::min<long long>(items, 0x7fffffff));

@@ -4,17 +4,19 @@
 //
 // A CTA takes one sequence, one K/V head and TILES x 128 of its query rows (the
 // group's heads times the call's tokens, so that the heads of a group share the
-// unpacked K and V), and walks over tiles of BN keys:
+// unpacked K and V), and walks over tiles of 64 keys:
 //   unpack warps   codes and scales -> fp16 K and V tiles in shared memory
-//   MMA warp       S_t = Q_t K^T, O_t += P_t V (fp32 in tensor memory)
+//   MMA warps      one a row tile: S = Q K^T, O += P V (fp32 in tensor memory);
+//                  a single one spent half of its time between the products
+//                  (waits, commits), with nothing queued
 //   softmax warps  thread = row = TMEM lane: S -> P (fp16, over S), the
-//                  running maximum, O's rescaling, the row sum.  S is read in
-//                  quarters, the next one while one is worked on.  The last
-//                  two stay in registers from the maximum to the exponentials, and P
-//                  goes over the second half of S, so that the first two can be read again.
-// D <= 128: two row tiles that take turns on the tensor pipe (S_A, S_B, then
-// P_A V, S_A of the next keys, P_B V, ...).  D > 128: one row tile, as two O
-// tiles do not fit, with two S buffers (S of the next keys runs beside the softmax).
+//                  running maximum, O's rescaling, the row sum
+// Each row tile has two S buffers, and S runs two key tiles ahead: a softmax
+// finds its next S ready, and the products are not on its way.  (With
+// tiles of 128 keys and one buffer, S of a row tile had to wait for its P V and that
+// for its P: softmax and products of a row tile took turns, 4500 cycles for
+// 128 keys, although each of the two needs half of that.)  D <= 128: two row
+// tiles; D > 128: one, as two O tiles do not fit the tensor memory.
 //
 // Numbers.  A value is s (n - 8) with s of 8 bits and n - 8 of 3, so K and V
 // are exact in fp16 once their scales are brought near one: each tile has
@@ -44,7 +46,8 @@
 namespace kv4 {
 
 constexpr int kRowTile = 128;
-constexpr int kInfo = 4;               // tile descriptions in flight
+constexpr int kKeys = 64;              // of a key tile, S's and P's
+constexpr int kInfo = 4;               // descriptions of unpacked groups in flight
 constexpr float kPHead = 7.f;          // P is held as p 2^kPHead, p <= 2^kLazy
 
 template <int NG>
@@ -52,20 +55,29 @@ struct Prompt {
     static constexpr int D = NG * kGroup;
     static constexpr bool kWide = NG > 4;
     static constexpr int TILES = kWide ? 1 : 2;
-    static constexpr int BN = kWide ? 64 : 128;
+    static constexpr int SUB = kWide ? 1 : 2;              // key tiles that are unpacked together, a group
+    static constexpr int kSlots = 2;                       // groups of K, and of V, in shared memory
+    static constexpr int kGroupKeys = SUB * kKeys;
     static constexpr int kBoxes = (NG + 1) / 2;            // 64 columns each
     static constexpr int N = kBoxes * 64;                  // columns of O (past D: zeros)
     static constexpr int kSoftWarps = 4 * TILES;
-    static constexpr int kUnpackWarps = kWide ? 8 : 4;
+    static constexpr int kUnpackWarps = 8;
     static constexpr int kMmaWarp = kSoftWarps + kUnpackWarps;
-    static constexpr int kThreads = (kMmaWarp + 1) * 32;
-    static constexpr int kQBox = kRowTile * 128, kBox = BN * 128;   // bytes
+    static constexpr int kThreads = (kMmaWarp + TILES) * 32;
+    static constexpr int kQBox = kRowTile * 128, kBox = kKeys * 128;   // bytes
     static constexpr int kQTile = kBoxes * kQBox, kTile = kBoxes * kBox;
-    static constexpr int kOffK = TILES * kQTile, kOffV = kOffK + 2 * kTile, kOffBar = kOffV + 2 * kTile;
+    static constexpr int kOffK = TILES * kQTile, kOffV = kOffK + kSlots * SUB * kTile,
+                         kOffBar = kOffV + kSlots * SUB * kTile;
     static constexpr int kSmem = kOffBar + 2048 + 1024;    // and room to align
-    static constexpr uint32_t kO = 256;                    // TMEM: S at 0 and 128, O from here on
+    // Registers a thread (D <= 128): 18 warps start with 96 each; 8 x 112 + 8 x 80
+    // + 2 x 96 of the MMA warps is what they started with.
+    static constexpr int kLaunchRegs = 96, kSoftRegs = 112, kUnpackRegs = 80;
+    static_assert(kWide || kSoftWarps * kSoftRegs + kUnpackWarps * kUnpackRegs + TILES * kLaunchRegs <=
+                               (kThreads / 32) * kLaunchRegs, "register split");
+    static constexpr uint32_t kO = 256;                    // TMEM: S of row tile t at 128 t and 128 t + 64, O from here on
     static_assert(kO + TILES * N <= 512, "tensor memory");
     static_assert(kSmem <= 232448, "shared memory");
+    static_assert(kInfo > kSlots + 1, "descriptions outlive their groups");
 };
 
 struct TileInfo {
@@ -76,11 +88,12 @@ struct TileInfo {
 
 struct PromptBars {
     uint64_t q_full, full[2][2], empty[2][2];   // [K or V][slot]
-    uint64_t s_full[2], p_full[2], o_done, o_last, info[kInfo], drain;
+    uint64_t s_full[2][2], p_full[2][2];        // [row tile][buffer]
+    uint64_t o_done[2], o_last[2], info[kInfo], drain[2];
     TileInfo tile[kInfo];
-    uint32_t top[2][8];                  // of each unpack warp: largest scales, K below V
-    uint32_t gone[2][8];
-    uint8_t nan_groups[kInfo][128];      // of each key of V
+    uint32_t top[2][8];                  // of each unpack warp: the largest scale of K or V,
+    uint32_t gone[2][8];                 // the 16 keys that are not there, a NaN of V
+    uint8_t nan_groups[kInfo][2 * kKeys];   // of each key of V
     uint32_t tmem;
     int abort;
 };
@@ -119,20 +132,6 @@ __device__ __forceinline__ void tmem_ld_x8(uint32_t at, uint32_t* r) {
                  : "r"(at));
 }
 
-__device__ __forceinline__ void tmem_ld_x16(uint32_t at, uint32_t* r) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
-        "[%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(at));
-}
-template <int N>
-__device__ __forceinline__ void store_p(uint32_t at, const uint32_t* p) {
-    if constexpr (N == 16) fa::ptx::tmem_st_32x32b_x16(at, p);
-    else fa::ptx::tmem_st_32x32b_x8(at, p);
-}
-
 __device__ __forceinline__ float pow2(int e) {   // -126 <= e <= 127
     return __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
 }
@@ -162,7 +161,7 @@ __device__ __forceinline__ void unpack_unit(const Words<2 * NG>& raw, const Word
 template <int NG, bool BF16>
 __global__ void __launch_bounds__(Prompt<NG>::kThreads, 1) prompt_kernel(Cache c, Attend a, PromptPlan plan) {
     using L = Prompt<NG>;
-    constexpr int D = L::D, TILES = L::TILES, BN = L::BN, NB = L::kBoxes, N = L::N;
+    constexpr int D = L::D, TILES = L::TILES, BN = kKeys, NB = L::kBoxes, N = L::N, KS = L::kSlots, SUB = L::SUB, GK = L::kGroupKeys;
     constexpr bool WIDE = L::kWide;
     constexpr int R = TILES * kRowTile, kUnpackWarps = L::kUnpackWarps;
     extern __shared__ uint8_t smem_raw[];
@@ -184,27 +183,32 @@ __global__ void __launch_bounds__(Prompt<NG>::kThreads, 1) prompt_kernel(Cache c
     const Work w = work_of(c, a, b, R, tile == 0 && head == 0 && split == 0 && threadIdx.x == 0);
     if (tile >= w.tiles) return;
     const int rows = min(R, w.n * a.G - tile * R);
-    // key tiles that some row sees, and this split's share of them
+    // groups of keys that some row sees, and this split's share of them; the
+    // last group's second tile is left out where no row sees it
     const int pos0 = w.len - w.n + tile * R / a.G, pos1 = w.len - w.n + (tile * R + rows - 1) / a.G;
-    const int t_lo = a.window >= 0 ? max(0, pos0 - a.window) / BN : 0;
-    const int t_all = pos1 >= 0 ? pos1 / BN + 1 - t_lo : 0;
-    const int jb = t_lo + static_cast<int>(static_cast<long long>(t_all) * split / splits);
-    const int n_tiles = t_lo + static_cast<int>(static_cast<long long>(t_all) * (split + 1) / splits) - jb;
+    const int g_lo = a.window >= 0 ? max(0, pos0 - a.window) / GK : 0;
+    const int g_all = pos1 >= 0 ? pos1 / GK + 1 - g_lo : 0;
+    const int gb = g_lo + static_cast<int>(static_cast<long long>(g_all) * split / splits);        // first group
+    const int n_groups = g_lo + static_cast<int>(static_cast<long long>(g_all) * (split + 1) / splits) - gb;
+    const int jb = gb * SUB;                                                                       // first key tile
+    const int n_tiles = max(0, min(n_groups * SUB, pos1 / kKeys + 1 - jb));
 
     if (threadIdx.x == 0) {
         fa::ptx::mbar_init(bar(&bars->q_full), R);
-        for (int i = 0; i < 2; ++i) {
-            for (int x = 0; x < 2; ++x) {
+        for (int x = 0; x < 2; ++x) {
+            for (int i = 0; i < KS; ++i) {
                 fa::ptx::mbar_init(bar(&bars->full[x][i]), kUnpackWarps);
-                fa::ptx::mbar_init(bar(&bars->empty[x][i]), 1);
+                fa::ptx::mbar_init(bar(&bars->empty[x][i]), TILES);
             }
-            fa::ptx::mbar_init(bar(&bars->s_full[i]), 1);
-            fa::ptx::mbar_init(bar(&bars->p_full[i]), kRowTile);
+            for (int i = 0; i < 2; ++i) {
+                fa::ptx::mbar_init(bar(&bars->s_full[x][i]), 1);
+                fa::ptx::mbar_init(bar(&bars->p_full[x][i]), kRowTile);
+            }
+            fa::ptx::mbar_init(bar(&bars->o_done[x]), 1);
+            fa::ptx::mbar_init(bar(&bars->o_last[x]), 1);
+            fa::ptx::mbar_init(bar(&bars->drain[x]), 1);
         }
         for (int i = 0; i < kInfo; ++i) fa::ptx::mbar_init(bar(&bars->info[i]), 1);
-        fa::ptx::mbar_init(bar(&bars->o_done), 1);
-        fa::ptx::mbar_init(bar(&bars->o_last), 1);
-        fa::ptx::mbar_init(bar(&bars->drain), 1);
         bars->abort = 0;
         fa::ptx::fence_barrier_init();
     }
@@ -222,7 +226,7 @@ __global__ void __launch_bounds__(Prompt<NG>::kThreads, 1) prompt_kernel(Cache c
         return __all_sync(0xffffffffu, wait_bar(b_, parity, abort, heed));
     };
 
-    if (warp == L::kMmaWarp) {
+    if (warp >= L::kMmaWarp) {
         // ------------------------------------------------------ MMA issue
         constexpr uint32_t kIdescS = fa::ptx::idesc_f16_f32(kRowTile, BN, false, false);
         constexpr uint32_t kIdescO = fa::ptx::idesc_f16_f32(kRowTile, N, false, true);
@@ -231,119 +235,107 @@ __global__ void __launch_bounds__(Prompt<NG>::kThreads, 1) prompt_kernel(Cache c
         const uint32_t klo = fa::ptx::sdesc_sw128_lo(sbase + L::kOffK, 16);
         const uint32_t vlo = fa::ptx::sdesc_sw128_lo(sbase + L::kOffV, L::kBox);
         bool ok = n_tiles == 0 || wait_warp(bar(&bars->q_full), 0);
-        // S of key tile j, row tile t, into buffer s: K steps of 16 elements, 4 to a box
-        auto issue_s = [&](int j, int t, int s) {
-            const uint32_t k = klo + (j & 1) * (L::kTile / 16), q = qlo + t * (L::kQTile / 16);
-            fa::ptx::tc_fence_after_sync();
+        const int t = warp - L::kMmaWarp;
+        const uint32_t q = qlo + t * (L::kQTile / 16);
+        // j = -2, -1: S of the first two key tiles alone
+        for (int j = -2; j < n_tiles && ok; ++j) {
+            if (j >= 0) {
+                // O from P of key tile j (16 keys in 8 columns), and from what P's rounding left
+                ok = wait_warp(bar(&bars->p_full[t][j & 1]), static_cast<uint32_t>((j >> 1) & 1));
+                if (ok && j % SUB == 0)
+                    ok = wait_warp(bar(&bars->full[1][j / SUB % KS]), static_cast<uint32_t>((j / (SUB * KS)) & 1));
+                if (!ok) break;
+                fa::ptx::tc_fence_after_sync();
+                const uint32_t v = vlo + (j % (KS * SUB)) * (L::kTile / 16), p = tmem + t * 128 + (j & 1) * 64;
 #pragma unroll
-            for (int x = 0; x < 2 * NG; x += 4) {
-                if (x + 4 <= 2 * NG) {
-                    fa::ptx::mma_ss_x4_lo(tmem + s * 128, q + (x / 4) * (L::kQBox / 16), k + (x / 4) * (L::kBox / 16), hi,
-                                          2u, kIdescS, x > 0 ? 1u : 0u);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 2; ++i)   // half a box is left
-                        fa::ptx::mma_ss_warp_lo(tmem + s * 128, q + (x / 4) * (L::kQBox / 16) + 2 * i,
-                                                k + (x / 4) * (L::kBox / 16) + 2 * i, hi, kIdescS, x + i > 0 ? 1u : 0u);
-                }
+                for (int part = 0; part < (BF16 ? 1 : 2); ++part)
+                    fa::ptx::mma_ts_x4_lo(tmem + L::kO + t * N, p + part * (BN / 2), v, hi, 8u, 128u, kIdescO,
+                                          (j > 0 || part > 0) ? 1u : 0u);
             }
-            fa::ptx::tc_commit_warp(bar(&bars->s_full[s]));
-        };
-        // O of row tile t from P in buffer s (8 columns a K step of 16 keys)
-        auto issue_o = [&](int j, int t, int s) {
-            const uint32_t v = vlo + (j & 1) * (L::kTile / 16);
-            fa::ptx::tc_fence_after_sync();
+            const int i = j + 2;
+            if (i < n_tiles) {
+                // S of key tile i into buffer i % 2 (P of j lay there): K steps of 16 elements, 4 to a box
+                if (i % SUB == 0) {
+                    ok = wait_warp(bar(&bars->full[0][i / SUB % KS]), static_cast<uint32_t>((i / (SUB * KS)) & 1));
+                    if (!ok) break;
+                    fa::ptx::tc_fence_after_sync();
+                }
+                const uint32_t d = tmem + t * 128 + (i & 1) * 64, k = klo + (i % (KS * SUB)) * (L::kTile / 16);
 #pragma unroll
-            for (int part = 0; part < (BF16 ? 1 : 2); ++part)     // and what P's rounding left
+                for (int x = 0; x < 2 * NG; x += 4) {
+                    if (x + 4 <= 2 * NG) {
+                        fa::ptx::mma_ss_x4_lo(d, q + (x / 4) * (L::kQBox / 16), k + (x / 4) * (L::kBox / 16), hi, 2u,
+                                              kIdescS, x > 0 ? 1u : 0u);
+                    } else {
 #pragma unroll
-                for (int x = 0; x < BN / 16; x += 4)
-                    fa::ptx::mma_ts_x4_lo(tmem + L::kO + t * N, tmem + s * 128 + (1 - part) * (BN / 2) + x * 8, v + x * 128, hi, 8u,
-                                          128u, kIdescO, (j > 0 || x > 0 || part > 0) ? 1u : 0u);
-        };
-        if constexpr (!WIDE) {
-            // j = -1: S of the first tile alone
-            for (int j = -1; j < n_tiles && ok; ++j) {
-#pragma unroll 1
-                for (int t = 0; t < TILES; ++t) {
-                  if (j >= 0) {
-                    if (!(ok = wait_warp(bar(&bars->p_full[t]), static_cast<uint32_t>(j & 1)))) break;
-                    if (t == 0 && !(ok = wait_warp(bar(&bars->full[1][j & 1]), static_cast<uint32_t>((j >> 1) & 1)))) break;
-                    issue_o(j, t, t);
-                    if (t == TILES - 1) {
-                        fa::ptx::tc_commit_warp(bar(&bars->empty[1][j & 1]));
-                        if (j + 1 == n_tiles) fa::ptx::tc_commit_warp(bar(&bars->o_last));
-                    }
-                  }
-                    if (j + 1 < n_tiles) {
-                        if (t == 0 &&
-                            !(ok = wait_warp(bar(&bars->full[0][(j + 1) & 1]), static_cast<uint32_t>(((j + 1) >> 1) & 1))))
-                            break;
-                        issue_s(j + 1, t, t);
-                        if (t == TILES - 1) fa::ptx::tc_commit_warp(bar(&bars->empty[0][(j + 1) & 1]));
+                        for (int e = 0; e < 2; ++e)   // half a box is left
+                            fa::ptx::mma_ss_warp_lo(d, q + (x / 4) * (L::kQBox / 16) + 2 * e,
+                                                    k + (x / 4) * (L::kBox / 16) + 2 * e, hi, kIdescS, x + e > 0 ? 1u : 0u);
                     }
                 }
+                fa::ptx::tc_commit_warp(bar(&bars->s_full[t][i & 1]));
+                if (i % SUB == SUB - 1) fa::ptx::tc_commit_warp(bar(&bars->empty[0][i / SUB % KS]));
             }
-        } else {
-            for (int j = -1; j < n_tiles && ok; ++j) {
-                if (j + 1 < n_tiles) {
-                    const int i = j + 1;
-                    if (!(ok = wait_warp(bar(&bars->full[0][i & 1]), static_cast<uint32_t>((i >> 1) & 1)))) break;
-                    issue_s(i, 0, i & 1);
-                    fa::ptx::tc_commit_warp(bar(&bars->empty[0][i & 1]));
-                }
-                if (j < 0) continue;
-                if (!(ok = wait_warp(bar(&bars->p_full[j & 1]), static_cast<uint32_t>((j >> 1) & 1)))) break;
-                if (!(ok = wait_warp(bar(&bars->full[1][j & 1]), static_cast<uint32_t>((j >> 1) & 1)))) break;
-                issue_o(j, 0, j & 1);
-                fa::ptx::tc_commit_warp(bar(&bars->empty[1][j & 1]));
-                fa::ptx::tc_commit_warp(bar(&bars->o_done));
-                if (j + 1 == n_tiles) fa::ptx::tc_commit_warp(bar(&bars->o_last));
+            if (j >= 0) {
+                // (these report S of j + 2 along with P V of j)
+                fa::ptx::tc_commit_warp(bar(&bars->o_done[t]));
+                if (j % SUB == SUB - 1) fa::ptx::tc_commit_warp(bar(&bars->empty[1][j / SUB % KS]));
+                if (j + 1 == n_tiles) fa::ptx::tc_commit_warp(bar(&bars->o_last[t]));
             }
         }
         // every MMA must be complete before the tensor memory is freed
-        fa::ptx::tc_commit_warp(bar(&bars->drain));
-        wait_warp(bar(&bars->drain), 0, false);
+        fa::ptx::tc_commit_warp(bar(&bars->drain[t]));
+        wait_warp(bar(&bars->drain[t]), 0, false);
     } else if (warp >= L::kSoftWarps) {
         // ---------------------------------------------------------- unpack
-        constexpr int CU = BN * 4 / (kUnpackWarps * 32);   // of the 4 units (c = 0 .. 3) of a key
+        if constexpr (!WIDE) fa::ptx::setmaxnreg_dec<L::kUnpackRegs>();
+        constexpr int CU = GK / 64;                        // units of this thread, of the 4 (c = 0 .. 3) of a key
         const int u = static_cast<int>(threadIdx.x) - L::kSoftWarps * 32;
-        const int key = u % BN, c0 = u / BN * CU;          // this thread's units: c0 .. c0 + CU - 1
+        const int key = u % GK, c0 = u / GK * CU;          // its units: c0 .. c0 + CU - 1
         const int uw = u >> 5;
+        const bool for_v = u / GK % 2 == 1;                // looks at V's scales (else at K's)
         const long long k_to_v = static_cast<long long>(c.Hkv) * c.P;   // rows
         if constexpr (NG % 2 == 1) {
             // the last box's right half is never written: columns of zeros
-            for (int i = u; i < 2 * BN * 4; i += kUnpackWarps * 32) {
+            for (int i = u; i < KS * SUB * BN * 4; i += kUnpackWarps * 32) {
                 const int st = i / (BN * 4), k = (i / 4) % BN, chunk = 4 + (i & 3);
                 *reinterpret_cast<uint4*>(smem + L::kOffV + st * L::kTile + (NB - 1) * L::kBox + k * 128 +
                                           ((chunk ^ (k & 7)) << 4)) = make_uint4(0, 0, 0, 0);
             }
         }
         const int* table = c.table + static_cast<long long>(b) * c.max_pages;
-        // K's rows of a tile, V's, K's of the next one, ...: each asked for as the
-        // ones before them are unpacked; the scales a tile ahead, the page two.
-        Words<2 * NG> raw[CU];
+        // Rows and scales are asked for a tile ahead (a half tile's unpacking
+        // is shorter than their latency), the page two.
+        Words<2 * NG> raw[2][CU], ahead[2][CU];   // K's and V's
         Words<NG> ks, vs, ks2, vs2;
-        long long row = -1, row2 = -1;   // of the key in the cache, this tile and the next; -1: none
         bool gone = false, gone2 = false;
-        int next = jb * BN + key;   // position that `pg`, `off` and `page` stand for
-        int pg = next / c.P, off = next - pg * c.P, page = -1, tile_at = 0;
-        const int step_pg = BN / c.P, step_off = BN - step_pg * c.P;
-        auto look_up = [&] { page = tile_at < n_tiles && next < w.len ? __ldg(table + pg) : -1; };
-        // the page of tile `tile_at` is here: its row, its scales; ask for the next page
+        int next = gb * GK + key;   // position that `pg`, `off` and `page` stand for
+        int pg = next / c.P, off = next - pg * c.P, page = -1, at_group = 0;
+        const int step_pg = GK / c.P, step_off = GK - step_pg * c.P;
+        auto look_up = [&] { page = at_group < n_groups && next < w.len ? __ldg(table + pg) : -1; };
+        // the page of group `at_group` is here: ask for its row and for the next page
         auto advance = [&] {
-            const bool mine = tile_at < n_tiles && next < w.len;
+            const bool mine = at_group < n_groups && next < w.len;
             const bool ok = mine && page >= 0 && page < c.pages;
             gone2 = mine && !ok;
             if (gone2) report(kStatusBadPages);
-            row2 = ok ? (static_cast<long long>(page) * 2 * c.Hkv + head) * c.P + off : -1;
             ks2.clear();
             vs2.clear();
+#pragma unroll
+            for (int i = 0; i < 2 * CU; ++i) ahead[i / CU][i % CU].clear();
             if (ok) {
-                ks2.load_global(c.scales + row2 * NG);
-                vs2.load_global(c.scales + (row2 + k_to_v) * NG);
+                const long long row = (static_cast<long long>(page) * 2 * c.Hkv + head) * c.P + off;
+                ks2.load_global(c.scales + row * NG);
+                vs2.load_global(c.scales + (row + k_to_v) * NG);
+                const uint8_t* codes = c.codes + row * (16 * NG) + c0 * (4 * NG);
+#pragma unroll
+                for (int i = 0; i < CU; ++i) {
+                    ahead[0][i].load_global(codes + i * (4 * NG));
+                    ahead[1][i].load_global(codes + k_to_v * (16 * NG) + i * (4 * NG));
+                }
             }
-            ++tile_at;
-            next += BN;
+            ++at_group;
+            next += GK;
             pg += step_pg;
             off += step_off;
             if (off >= c.P) {
@@ -352,94 +344,88 @@ __global__ void __launch_bounds__(Prompt<NG>::kThreads, 1) prompt_kernel(Cache c
             }
             look_up();
         };
-        auto load_rows = [&](Words<2 * NG>* to, long long from) {
-#pragma unroll
-            for (int i = 0; i < CU; ++i) {
-                to[i].clear();
-                if (from >= 0) to[i].load_global(c.codes + from * (16 * NG) + (c0 + i) * (4 * NG));
-            }
-        };
         look_up();
         advance();
-        load_rows(raw, row2);
         bool ok = true;
-        for (int j = 0; j < n_tiles; ++j) {
+        for (int g = 0; g < n_groups; ++g) {
             ks = ks2;
             vs = vs2;
             gone = gone2;
-            row = row2;
-            advance();
-            // ---- the tile's largest finite scales, NaNs and holes
-            uint32_t kt = 0, vt = 0, nan_groups = 0;
 #pragma unroll
-            for (int g = 0; g < NG; ++g) {
-                const uint32_t x = ks.get(g) & 0x7fffu, z = vs.get(g) & 0x7fffu;
-                kt = max(kt, x < 0x7f80u ? x : 0u);
-                if (z >= 0x7f80u) {
-                    nan_groups |= 1u << g;
-                    vs.set(g, 0);
-                } else {
-                    vt = max(vt, z);
-                }
+            for (int i = 0; i < 2 * CU; ++i) raw[i / CU][i % CU] = ahead[i / CU][i % CU];
+            advance();
+            // ---- the group's largest finite scales (half of the warps look at K's,
+            // half at V's), NaNs of V and holes
+            uint32_t most = 0, nan_groups = 0;
+#pragma unroll
+            for (int i = 0; i < NG; ++i) {
+                const uint32_t x = (for_v ? vs.get(i) : ks.get(i)) & 0x7fffu;
+                if (x >= 0x7f80u) nan_groups |= 1u << i;
+                most = max(most, x < 0x7f80u ? x : 0u);
             }
-            kt = __reduce_max_sync(0xffffffffu, kt);
-            vt = __reduce_max_sync(0xffffffffu, vt);
+            most = __reduce_max_sync(0xffffffffu, most);
             const uint32_t holes = __ballot_sync(0xffffffffu, gone);
-            const bool any_nan = __any_sync(0xffffffffu, nan_groups != 0);
-            // Slot j % kInfo is free: V of tile j - 1 waited for P V of j - 3, so the
-            // softmax is done with tile j - 4.
-            if (c0 == 0) bars->nan_groups[j % kInfo][key] = static_cast<uint8_t>(nan_groups);
+            const bool any_nan = for_v && __any_sync(0xffffffffu, nan_groups != 0);
+            // Slot g % kInfo is free: V of group g - 1 waited for P V of g - 1 - KS, so the
+            // softmax is done with that group and those before it.
+            if (u / GK == 1) bars->nan_groups[g % kInfo][key] = static_cast<uint8_t>(nan_groups);
             if (lane == 0) {
-                bars->top[j & 1][uw] = kt | (vt << 16);
-                bars->gone[j & 1][uw] = ((holes & 0xffffu) ? 1u : 0u) | ((holes >> 16) ? 2u : 0u) | (any_nan ? 4u : 0u);
+                bars->top[g & 1][uw] = for_v ? most << 16 : most;
+                bars->gone[g & 1][uw] = ((holes & 0xffffu) ? 1u : 0u) | ((holes >> 16) ? 2u : 0u) | (any_nan ? 4u : 0u);
             }
             fa::ptx::named_barrier_sync(2, kUnpackWarps * 32);
-            uint32_t top = 0;
+            uint32_t top = 0, flags = 0;
 #pragma unroll
-            for (int i = 0; i < kUnpackWarps; ++i) top = __vmaxu2(top, bars->top[j & 1][i]);
+            for (int i = 0; i < kUnpackWarps; ++i) {
+                top = __vmaxu2(top, bars->top[g & 1][i]);
+                flags |= bars->gone[g & 1][i];
+            }
             // largest scale 2^e (1 .. 2) -> 2^11 .. 2^12
             const int ek = max(static_cast<int>((top & 0xffffu) >> 7) - 127, -100) - 11;
             const int ev = max(static_cast<int>(top >> 23) - 127, -100) - 11;
             if (u == 0) {   // what the softmax has to know
-                uint32_t missing = 0, flags = 0;
-                for (int i = 0; i < kUnpackWarps; ++i) {
-                    const uint32_t f = bars->gone[j & 1][i];
-                    flags |= f & 4u;
-                    missing |= (f & 3u) << (2 * (i % (BN / 32)));
-                }
-                bars->tile[j % kInfo] = {ek, ev, missing, flags};
-                fa::ptx::mbar_arrive(bar(&bars->info[j % kInfo]));
+                uint32_t missing = 0;
+                if (flags & 3u)
+                    for (int i = 0; i < kUnpackWarps; ++i) missing |= (bars->gone[g & 1][i] & 3u) << (2 * (i % (GK / 32)));
+                bars->tile[g % kInfo] = {ek, ev, missing, flags & 4u};
+                fa::ptx::mbar_arrive(bar(&bars->info[g % kInfo]));
+            }
+            if (flags & 4u) {   // NaNs of V stay out of the products
+#pragma unroll
+                for (int i = 0; i < NG; ++i)
+                    if ((vs.get(i) & 0x7fffu) >= 0x7f80u) vs.set(i, 0);
             }
             // ---- K, then V, each once its slot is free
 #pragma unroll 1
             for (int x = 0; x < 2; ++x) {
-                if (j >= 2)
-                    ok = ok && wait_warp(bar(&bars->empty[x][j & 1]), static_cast<uint32_t>(((j >> 1) - 1) & 1));
-                Words<2 * NG> ahead[CU];
-                load_rows(ahead, x == 0 ? (row < 0 ? -1 : row + k_to_v) : row2);
+                if (g >= KS)
+                    ok = ok && wait_warp(bar(&bars->empty[x][g % KS]), static_cast<uint32_t>((g / KS - 1) & 1));
                 if (ok) {
-                    uint8_t* to = smem + (x == 0 ? L::kOffK : L::kOffV) + (j & 1) * L::kTile;
+                    uint8_t* to = smem + (x == 0 ? L::kOffK : L::kOffV) + (g % KS * SUB + key / kKeys) * L::kTile;
                     const float down = pow2(x == 0 ? -ek : -ev);
 #pragma unroll
-                    for (int i = 0; i < CU; ++i) unpack_unit<NG, L::kBox>(raw[i], ks, down, c0 + i, key, to);
+                    for (int i = 0; i < CU; ++i)
+                        unpack_unit<NG, L::kBox>(raw[0][i], ks, down, c0 + i, key % kKeys, to);
                     fa::ptx::fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane == 0) fa::ptx::mbar_arrive(bar(&bars->full[x][j & 1]));
+                    if (lane == 0) fa::ptx::mbar_arrive(bar(&bars->full[x][g % KS]));
                 }
                 ks = vs;
 #pragma unroll
-                for (int i = 0; i < CU; ++i) raw[i] = ahead[i];
+                for (int i = 0; i < CU; ++i) raw[0][i] = raw[1][i];
             }
         }
     } else {
         // --------------------------------------------------------- softmax
+        if constexpr (!WIDE) fa::ptx::setmaxnreg_inc<L::kSoftRegs>();
         const int t = warp >> 2;                                      // row tile
         const int r = static_cast<int>(threadIdx.x) & 127;            // row of the tile, TMEM lane
         const int row = t * kRowTile + r, rho = tile * R + row;
         const bool real = row < rows;
         const int qi = rho / a.G, h = head * a.G + rho - qi * a.G;
-        const int pos = real ? w.len - w.n + qi : -1;
-        const int first = a.window >= 0 ? max(0, pos - a.window) : 0;
+        // rows past the last one see everything (their Q is 0), so that they need no mask
+        const int pos = real ? w.len - w.n + qi : 0x7fffffff;
+        const int first = real && a.window >= 0 ? max(0, pos - a.window) : 0;
         const uint32_t lane_off = static_cast<uint32_t>(32 * (warp & 3)) << 16;
         float f;   // z = S 2^Ek f
         {
@@ -481,28 +467,18 @@ __global__ void __launch_bounds__(Prompt<NG>::kThreads, 1) prompt_kernel(Cache c
         uint32_t poison = 0;      // groups that met a NaN of V
         bool ok = true;
         for (int j = 0; j < n_tiles; ++j) {
-            const int sb = WIDE ? (j & 1) : t;
-            const uint32_t phase = WIDE ? static_cast<uint32_t>((j >> 1) & 1) : static_cast<uint32_t>(j & 1);
-            ok = ok && wait_bar(bar(&bars->s_full[sb]), phase, abort) &&
-                 wait_bar(bar(&bars->info[j % kInfo]), static_cast<uint32_t>((j / kInfo) & 1), abort);
+            const int g = j / SUB;
+            ok = ok && (j % SUB != 0 || wait_bar(bar(&bars->info[g % kInfo]), static_cast<uint32_t>((g / kInfo) & 1), abort)) &&
+                 wait_bar(bar(&bars->s_full[t][j & 1]), static_cast<uint32_t>((j >> 1) & 1), abort);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             fa::ptx::tc_fence_after_sync();
-            const TileInfo info = bars->tile[j % kInfo];
-            const uint32_t tS = tmem + lane_off + sb * 128;
+            const TileInfo info = bars->tile[g % kInfo];
+            const uint32_t tS = tmem + lane_off + t * 128 + (j & 1) * 64;
             const int kv0 = (jb + j) * BN;
-            const uint32_t missing = info.missing;
-            const bool edge = __any_sync(0xffffffffu, kv0 + BN - 1 > pos || kv0 < first || missing != 0);
+            const uint32_t missing = info.missing >> (j % SUB * (kKeys / 16));
+            const bool edge = __any_sync(0xffffffffu, kv0 + BN - 1 > pos || kv0 < first || (missing & 15u) != 0);
             const float zf = f * pow2(info.ek), ev = static_cast<float>(info.ev);
-            constexpr int QK = BN / 4;   // keys of a quarter
-            auto read = [&](uint32_t* s, int q) {
-                if constexpr (QK == 32) fa::ptx::tmem_ld_32x32b_x32(tS + q * QK, s);
-                else tmem_ld_x16(tS + q * QK, s);
-            };
-            auto arrived = [&](uint32_t* s, int q) {
-                fa::ptx::tmem_ld_wait();
-                fa::ptx::reg_fence<QK>(s);
-            };
             if (edge) {
                 // masked scores become -inf where they are
 #pragma unroll 1
@@ -521,20 +497,17 @@ __global__ void __launch_bounds__(Prompt<NG>::kThreads, 1) prompt_kernel(Cache c
                 }
                 fa::ptx::tmem_st_wait();
             }
-            uint32_t buf[2][QK];
+            uint32_t sv[BN];
+            fa::ptx::tmem_ld_32x32b_x32(tS, sv);
+            fa::ptx::tmem_ld_32x32b_x32(tS + 32, sv + 32);
+            fa::ptx::tmem_ld_wait();
+            fa::ptx::reg_fence<BN>(sv);
             float mx[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
-            read(buf[0], 0);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                arrived(buf[q & 1], q);
-                if (q < 3) read(buf[(q + 1) & 1], q + 1);
-                uint32_t* s = buf[q & 1];
+            for (int k = 0; k < BN; k += 8)
 #pragma unroll
-                for (int k = 0; k < QK; k += 8)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        mx[i] = fa::ptx::fmax3(mx[i], __uint_as_float(s[k + 2 * i]), __uint_as_float(s[k + 2 * i + 1]));
-            }
+                for (int i = 0; i < 4; ++i)
+                    mx[i] = fa::ptx::fmax3(mx[i], __uint_as_float(sv[k + 2 * i]), __uint_as_float(sv[k + 2 * i + 1]));
             mx[0] = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
             // the reference moves lazily, when p' would pass 2^kLazy
             const float top = mx[0] == kNegInf ? kNegInf : fmaf(mx[0], zf, ev);
@@ -545,13 +518,11 @@ __global__ void __launch_bounds__(Prompt<NG>::kThreads, 1) prompt_kernel(Cache c
                 ref = top;
             }
             if (j > 0 && __any_sync(0xffffffffu, move)) {
-                // S of this tile came after P V of the one before (D <= 128); else that has a barrier of its own
-                if constexpr (WIDE) {
-                    ok = wait_bar(bar(&bars->o_done), static_cast<uint32_t>((j - 1) & 1), abort);
-                    ok = __all_sync(0xffffffffu, ok);
-                    if (!ok) break;
-                    fa::ptx::tc_fence_after_sync();
-                }
+                // S of this tile came after P V of the tile two before; the one before has to be waited for
+                ok = wait_bar(bar(&bars->o_done[t]), static_cast<uint32_t>((j - 1) & 1), abort);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                fa::ptx::tc_fence_after_sync();
 #pragma unroll 1
                 for (int q = 0; q < N / 8; ++q) {   // few registers: the row of S is held
                     uint32_t o[8];
@@ -566,52 +537,38 @@ __global__ void __launch_bounds__(Prompt<NG>::kThreads, 1) prompt_kernel(Cache c
             if (info.nan != 0) {
                 for (int k = 0; k < BN; ++k) {
                     const int key = (jb + j) * BN + k;
-                    if (key <= pos && key >= first) poison |= bars->nan_groups[j % kInfo][k];
+                    if (key <= pos && key >= first) poison |= bars->nan_groups[g % kInfo][j % SUB * kKeys + k];
                 }
             }
             const float off = ev + kPHead - (ref == kNegInf ? 0.f : ref);
             const float2 zf2 = make_float2(zf, zf), off2 = make_float2(off, off);
             float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-            // the quarters 2, 3, 0, 1: P of q in columns BN / 2 + q QK / 2 on, what its
-            // rounding left in q QK / 2 on, which has to wait until S has been read there
-            uint32_t left[BF16 ? 1 : 2][QK / 2];
+            // P in the buffer's first half, what its rounding left in the second
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int q = (i + 2) & 3;
-                uint32_t* s = buf[i & 1];
-                if (i >= 2) {
-                    arrived(s, q);
-                    if constexpr (!BF16)
-                        if (i == 2) {   // the wait was for quarter 1 as well
+            for (int q = 0; q < BN / 32; ++q) {
+                uint32_t pk[16], left[16];
 #pragma unroll
-                            for (int h = 0; h < 2; ++h) store_p<QK / 2>(tS + (2 + h) * (QK / 2), left[h]);
-                        }
-                }
-                uint32_t pk[QK / 2];
-#pragma unroll
-                for (int k = 0; k < QK / 2; ++k) {
-                    const float2 x = __ffma2_rn(make_float2(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1])),
-                                                zf2, off2);
+                for (int k = 0; k < 16; ++k) {
+                    const float2 x = __ffma2_rn(make_float2(__uint_as_float(sv[q * 32 + 2 * k]),
+                                                            __uint_as_float(sv[q * 32 + 2 * k + 1])), zf2, off2);
                     const float2 p = make_float2(fa::ptx::ex2_approx(x.x), fa::ptx::ex2_approx(x.y));
                     sum[k & 1] = __fadd2_rn(sum[k & 1], p);
                     pk[k] = pack16<false>(p.x, p.y);
                     if constexpr (!BF16) {
                         const float2 got = to_f32x2<false>(pk[k]);
-                        left[i & 1][k] = pack16<false>(p.x - got.x, p.y - got.y);
+                        left[k] = pack16<false>(p.x - got.x, p.y - got.y);
                     }
                 }
-                if (i < 2) read(s, i);   // quarter 0 or 1 again
-                store_p<QK / 2>(tS + BN / 2 + q * (QK / 2), pk);
-                if constexpr (!BF16)
-                    if (i >= 2) store_p<QK / 2>(tS + q * (QK / 2), left[i & 1]);
+                fa::ptx::tmem_st_32x32b_x16(tS + q * 16, pk);
+                if constexpr (!BF16) fa::ptx::tmem_st_32x32b_x16(tS + BN / 2 + q * 16, left);
             }
             l = l * alpha + ((sum[0].x + sum[0].y) + (sum[1].x + sum[1].y)) * pow2(-info.ev);
             fa::ptx::tmem_st_wait();
             fa::ptx::tc_fence_before_sync();
-            fa::ptx::mbar_arrive(bar(&bars->p_full[sb]));
+            fa::ptx::mbar_arrive(bar(&bars->p_full[t][j & 1]));
         }
         // -------------------------------------------------------- epilogue
-        ok = ok && (n_tiles == 0 || wait_bar(bar(&bars->o_last), 0, abort));
+        ok = ok && (n_tiles == 0 || wait_bar(bar(&bars->o_last[t]), 0, abort));
         ok = __all_sync(0xffffffffu, ok);
         fa::ptx::tc_fence_after_sync();
         const float m = ref == kNegInf ? kNegInf : ref - kPHead;
