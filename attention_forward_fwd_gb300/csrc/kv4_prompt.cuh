@@ -91,8 +91,8 @@ struct PromptBars {
     uint64_t s_full[2][2], p_full[2][2];        // [row tile][buffer]
     uint64_t o_done[2], o_last[2], info[kInfo], drain[2];
     TileInfo tile[kInfo];
-    uint32_t top[2][8];                  // of each unpack warp: the largest scale of K or V,
-    uint32_t gone[2][8];                 // the 16 keys that are not there, a NaN of V
+    uint32_t top[3][2], flags[3];        // of a group: largest scales of K and V; bit i: 16 keys
+                                         // that are not there, bit 31: a NaN of V
     uint8_t nan_groups[kInfo][2 * kKeys];   // of each key of V
     uint32_t tmem;
     int abort;
@@ -108,11 +108,14 @@ struct PromptPlan {
 };
 
 // Bounded wait; false (and the CTA's abort flag set) when it ran out, or when
-// another role gave up.
-__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int* abort, bool heed = true) {
+// another role gave up.  `nap`: nanoseconds to sleep between probes, for warps
+// that have time, so that their asking takes no issue slots from the others.
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int* abort, bool heed = true,
+                                         unsigned nap = 0) {
     if (fa::ptx::mbar_try_wait(bar, parity)) return true;
     const uint64_t t0 = fa::ptx::globaltimer();
     for (uint32_t n = 1;; ++n) {
+        if (nap != 0) __nanosleep(nap);
         if (fa::ptx::mbar_try_wait(bar, parity)) return true;
         if ((n & 31u) == 0) {
             if (heed && *abort) return false;
@@ -209,6 +212,7 @@ __global__ void __launch_bounds__(Prompt<NG>::kThreads, 1) prompt_kernel(Cache c
             fa::ptx::mbar_init(bar(&bars->drain[x]), 1);
         }
         for (int i = 0; i < kInfo; ++i) fa::ptx::mbar_init(bar(&bars->info[i]), 1);
+        for (int i = 0; i < 3; ++i) bars->top[i][0] = bars->top[i][1] = bars->flags[i] = 0;
         bars->abort = 0;
         fa::ptx::fence_barrier_init();
     }
@@ -222,8 +226,8 @@ __global__ void __launch_bounds__(Prompt<NG>::kThreads, 1) prompt_kernel(Cache c
     const uint32_t tmem = bars->tmem;
     fa::ptx::launch_dependents();
 
-    auto wait_warp = [&](uint32_t b_, uint32_t parity, bool heed = true) {
-        return __all_sync(0xffffffffu, wait_bar(b_, parity, abort, heed));
+    auto wait_warp = [&](uint32_t b_, uint32_t parity, bool heed = true, unsigned nap = 0) {
+        return __all_sync(0xffffffffu, wait_bar(b_, parity, abort, heed, nap));
     };
 
     if (warp >= L::kMmaWarp) {
@@ -347,6 +351,7 @@ __global__ void __launch_bounds__(Prompt<NG>::kThreads, 1) prompt_kernel(Cache c
         look_up();
         advance();
         bool ok = true;
+        int at3 = 0;   // g % 3
         for (int g = 0; g < n_groups; ++g) {
             ks = ks2;
             vs = vs2;
@@ -370,27 +375,24 @@ __global__ void __launch_bounds__(Prompt<NG>::kThreads, 1) prompt_kernel(Cache c
             // softmax is done with that group and those before it.
             if (u / GK == 1) bars->nan_groups[g % kInfo][key] = static_cast<uint8_t>(nan_groups);
             if (lane == 0) {
-                bars->top[g & 1][uw] = for_v ? most << 16 : most;
-                bars->gone[g & 1][uw] = ((holes & 0xffffu) ? 1u : 0u) | ((holes >> 16) ? 2u : 0u) | (any_nan ? 4u : 0u);
+                atomicMax(&bars->top[at3][for_v ? 1 : 0], most);
+                const uint32_t f = ((holes & 0xffffu) ? 1u : 0u) | ((holes >> 16) ? 2u : 0u);
+                if (f != 0 || any_nan) atomicOr(&bars->flags[at3], f << (2 * (uw % (GK / 32))) | (any_nan ? 1u << 31 : 0u));
             }
             fa::ptx::named_barrier_sync(2, kUnpackWarps * 32);
-            uint32_t top = 0, flags = 0;
-#pragma unroll
-            for (int i = 0; i < kUnpackWarps; ++i) {
-                top = __vmaxu2(top, bars->top[g & 1][i]);
-                flags |= bars->gone[g & 1][i];
-            }
+            const uint32_t top_k = bars->top[at3][0], top_v = bars->top[at3][1], flags = bars->flags[at3];
+            at3 = at3 == 2 ? 0 : at3 + 1;
+            // (the slot of the group before is cleared below: everyone read it before this barrier)
             // largest scale 2^e (1 .. 2) -> 2^11 .. 2^12
-            const int ek = max(static_cast<int>((top & 0xffffu) >> 7) - 127, -100) - 11;
-            const int ev = max(static_cast<int>(top >> 23) - 127, -100) - 11;
+            const int ek = max(static_cast<int>(top_k >> 7) - 127, -100) - 11;
+            const int ev = max(static_cast<int>(top_v >> 7) - 127, -100) - 11;
             if (u == 0) {   // what the softmax has to know
-                uint32_t missing = 0;
-                if (flags & 3u)
-                    for (int i = 0; i < kUnpackWarps; ++i) missing |= (bars->gone[g & 1][i] & 3u) << (2 * (i % (GK / 32)));
-                bars->tile[g % kInfo] = {ek, ev, missing, flags & 4u};
+                const int clear = at3 == 2 ? 0 : at3 + 1;
+                bars->top[clear][0] = bars->top[clear][1] = bars->flags[clear] = 0;
+                bars->tile[g % kInfo] = {ek, ev, flags & 0x7fffffffu, flags >> 31};
                 fa::ptx::mbar_arrive(bar(&bars->info[g % kInfo]));
             }
-            if (flags & 4u) {   // NaNs of V stay out of the products
+            if (flags >> 31) {   // NaNs of V stay out of the products
 #pragma unroll
                 for (int i = 0; i < NG; ++i)
                     if ((vs.get(i) & 0x7fffu) >= 0x7f80u) vs.set(i, 0);
@@ -399,7 +401,7 @@ __global__ void __launch_bounds__(Prompt<NG>::kThreads, 1) prompt_kernel(Cache c
 #pragma unroll 1
             for (int x = 0; x < 2; ++x) {
                 if (g >= KS)
-                    ok = ok && wait_warp(bar(&bars->empty[x][g % KS]), static_cast<uint32_t>((g / KS - 1) & 1));
+                    ok = ok && wait_warp(bar(&bars->empty[x][g % KS]), static_cast<uint32_t>((g / KS - 1) & 1), true, 100);
                 if (ok) {
                     uint8_t* to = smem + (x == 0 ? L::kOffK : L::kOffV) + (g % KS * SUB + key / kKeys) * L::kTile;
                     const float down = pow2(x == 0 ? -ek : -ev);
