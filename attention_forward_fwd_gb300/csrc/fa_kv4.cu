@@ -148,7 +148,7 @@ int decode(const kv4::Cache& c, kv4::Attend a, void* ws, size_t ws_bytes, Decode
     pdl[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(plan.items_most) * c.B);
-    cfg.blockDim = dim3(kv4::kWarps * 32);
+    cfg.blockDim = dim3(kv4::kJoinWarps * 32);
     cfg.stream = st;
     cfg.attrs = pdl;
     cfg.numAttrs = 1;
@@ -157,8 +157,12 @@ int decode(const kv4::Cache& c, kv4::Attend a, void* ws, size_t ws_bytes, Decode
 }
 
 // Query rows a K/V head (the group's heads times the call's tokens) up to
-// which decode_kernel takes a call.
-constexpr int kDecodeRows = 16;
+// which decode_kernel takes a call: it reads the cache once for every 8 or 16
+// rows, prompt_kernel once for 128 or 256, for the price of that many.  us at 32 /
+// 64 rows, decode against prompt: 16 x 8192 keys, 8 heads, D = 64 84 / 150
+// against 131, D = 128 113 / 199 against 139, D = 256 236 / 449 against 318; 64 x 2048
+// keys, D = 128 117 / 192 against 106.
+constexpr int kDecodeRows = 32;
 
 template <int NG, bool BF16>
 int prompt(const kv4::Cache& c, kv4::Attend a, void* ws, size_t ws_bytes, DecodePlan* only_plan, cudaStream_t st) {

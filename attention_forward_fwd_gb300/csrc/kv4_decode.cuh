@@ -821,73 +821,105 @@ __global__ void __launch_bounds__(kThreads, NG <= 4 && NT == 1 ? 3 : 2) decode_k
     }
 }
 
-// Joins the parts of the items that the ranges of decode_kernel cut: one CTA
-// an item, in the order of the keys (the result does not depend on which CTA
-// ended first).
+// Joins the parts of the items that the ranges of decode_kernel cut: a CTA an
+// item, a warp for each eighth row, lanes over the row's elements; in the
+// order of the keys, so that the result does not depend on which CTA ended
+// first.  All parts' references are read at once, then eight parts' elements at a
+// time (one after the other, a context of 32768 keys took 25 us here).
+constexpr int kJoinWarps = 8;
+
 template <int NG, int NT, bool BF16>
-__global__ void __launch_bounds__(kWarps * 32) combine_kernel(Cache c, Attend a, int items_most) {
-    constexpr int D = NG * kGroup, R = 8 * NT;
-    __shared__ long long two[2][kWarps];
+__global__ void __launch_bounds__(kJoinWarps * 32) combine_kernel(Cache c, Attend a, int items_most) {
+    constexpr int D = NG * kGroup, R = 8 * NT, E4 = (D / 4 + 31) / 32;   // float4s of a lane
+    __shared__ long long two[2][kJoinWarps];
     const int b = blockIdx.x / items_most, item = blockIdx.x - b * items_most;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const Work w = work_of(c, a, b, R, false);
-    if (item >= w.items) {
-        fa::ptx::grid_dependency_wait();   // every CTA waits: this launch ends after the one before it
-        return;
-    }
     // blocks before sequence b, and of the whole call
     long long before = 0, all = 0;
-    {
-        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-        long long mine_all = 0, mine_before = 0;
+    if (item < w.items) {
         for (int i = threadIdx.x; i < c.B; i += blockDim.x) {
             const Work v = work_of(c, a, i, R, false);
             const long long k = static_cast<long long>(v.items) * v.blocks;
-            mine_all += k;
-            if (i < b) mine_before += k;
+            all += k;
+            if (i < b) before += k;
         }
 #pragma unroll
         for (int m = 16; m; m >>= 1) {
-            mine_all += __shfl_xor_sync(0xffffffffu, mine_all, m);
-            mine_before += __shfl_xor_sync(0xffffffffu, mine_before, m);
+            all += __shfl_xor_sync(0xffffffffu, all, m);
+            before += __shfl_xor_sync(0xffffffffu, before, m);
         }
         if (lane == 0) {
-            two[0][warp] = mine_all;
-            two[1][warp] = mine_before;
+            two[0][warp] = all;
+            two[1][warp] = before;
         }
         __syncthreads();
-        for (int i = 0; i < kWarps; ++i) {
+        all = before = 0;
+        for (int i = 0; i < kJoinWarps; ++i) {
             all += two[0][i];
             before += two[1][i];
         }
     }
+    fa::ptx::grid_dependency_wait();   // every CTA waits: this launch ends after the one before it
+    if (item >= w.items) return;
     const long long quota = quota_of(all, a.grid);
     const long long s = before + static_cast<long long>(item) * w.blocks, e = s + w.blocks;
-    const int first = static_cast<int>(s / quota), last = static_cast<int>((e - 1) / quota);
-    fa::ptx::grid_dependency_wait();
-    if (first == last) return;   // decode_kernel wrote it
+    const int first = static_cast<int>(s / quota), parts = static_cast<int>((e - 1) / quota) - first + 1;
+    if (parts == 1) return;   // decode_kernel wrote it
     const int head = item / w.tiles, tile = item - head * w.tiles;
     const int rows = min(R, w.n * a.G - tile * R);
-    for (int i = threadIdx.x; i < rows * (D / 4); i += kWarps * 32) {
-        const int rr = i / (D / 4), d4 = i - rr * (D / 4);
-        // the first part starts the item (slot 1 of its CTA), the others carry it on (slot 0)
+    // part k lies in slot 2 (first + k), or behind it for the one that starts the item
+    auto slot = [&](int k) { return 2 * (first + k) + (k == 0 ? 1 : 0); };
+    for (int rr = warp; rr < rows; rr += kJoinWarps) {
         float m = kNegInf, l = 0.f;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int k = first; k <= last; ++k) {
-            const int slot = 2 * k + (k == first ? 1 : 0);
-            const float2 ml = __ldcg(a.part_ml + slot * R + rr);
-            const float4 v = __ldcg(reinterpret_cast<const float4*>(
-                a.part_o + (static_cast<long long>(slot) * R + rr) * D + 4 * d4));
-            const float mn = fmaxf(m, ml.x);
-            if (mn == kNegInf) continue;
-            const float f0 = fa::ptx::ex2_approx(m - mn), f1 = fa::ptx::ex2_approx(ml.x - mn);
-            m = mn;
-            l = l * f0 + ml.y * f1;
-            o.x = o.x * f0 + v.x * f1;
-            o.y = o.y * f0 + v.y * f1;
-            o.z = o.z * f0 + v.z * f1;
-            o.w = o.w * f0 + v.w * f1;
+        for (int k = lane; k < parts; k += 32) m = fmaxf(m, __ldcg(a.part_ml + slot(k) * R + rr).x);
+#pragma unroll
+        for (int x = 16; x; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+        float4 o[E4];
+#pragma unroll
+        for (int i = 0; i < E4; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k0 = 0; k0 < parts; k0 += 32) {
+            // this lane's part of the next 32: its weight
+            float f = 0.f, fl = 0.f;
+            if (k0 + lane < parts) {
+                const float2 ml = __ldcg(a.part_ml + slot(k0 + lane) * R + rr);
+                f = ml.x == kNegInf ? 0.f : fa::ptx::ex2_approx(ml.x - m);
+                fl = f * ml.y;
+            }
+#pragma unroll
+            for (int x = 16; x; x >>= 1) fl += __shfl_xor_sync(0xffffffffu, fl, x);
+            l += fl;
+            const int n = min(32, parts - k0);
+#pragma unroll 1
+            for (int k = 0; k < n; k += 8) {
+                float4 v[8][E4];
+#pragma unroll
+                for (int x = 0; x < 8; ++x)
+#pragma unroll
+                    for (int i = 0; i < E4; ++i)
+                        v[x][i] = k + x < n && (D % 128 == 0 || i * 32 + lane < D / 4)
+                                      ? __ldcg(reinterpret_cast<const float4*>(
+                                                   a.part_o + (static_cast<long long>(slot(k0 + k + x)) * R + rr) * D) +
+                                               i * 32 + lane)
+                                      : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int x = 0; x < 8; ++x) {
+                    const float fx = __shfl_sync(0xffffffffu, f, k + x);
+#pragma unroll
+                    for (int i = 0; i < E4; ++i) {
+                        o[i].x += fx * v[x][i].x;
+                        o[i].y += fx * v[x][i].y;
+                        o[i].z += fx * v[x][i].z;
+                        o[i].w += fx * v[x][i].w;
+                    }
+                }
+            }
         }
-        write_row<BF16>(c, a, w, b, D, tile * R + rr, head, 4 * d4, o, m, l, d4 == 0 && a.lse != nullptr);
+#pragma unroll
+        for (int i = 0; i < E4; ++i)
+            if (D % 128 == 0 || i * 32 + lane < D / 4)
+                write_row<BF16>(c, a, w, b, D, tile * R + rr, head, 4 * (i * 32 + lane), o[i], m, l,
+                                i == 0 && lane == 0 && a.lse != nullptr);
     }
 }
 
