@@ -81,19 +81,19 @@ unsigned row_blocks(const kv4::Cache& c) {
 int launched() { return cudaPeekAtLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA; }
 
 // SMs of the current device and how many CTAs of `kernel` one holds, looked
-// up once for each device.
+// up once for each device; some launches may take `smem_more` bytes besides.
 struct Resident {
     std::once_flag once[kMaxDevices];
     int sms[kMaxDevices] = {}, ctas[kMaxDevices] = {};
 };
 
 template <typename Kernel>
-bool resident(Resident& r, Kernel* kernel, int threads, int smem, int* sms, int* ctas) {
+bool resident(Resident& r, Kernel* kernel, int threads, int smem, int* sms, int* ctas, int smem_more = 0) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return false;
     std::call_once(r.once[dev], [&] {
         int n = 0, k = 0;
-        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return;
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem + smem_more) != cudaSuccess) return;
         if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return;
         if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&k, kernel, threads, smem) != cudaSuccess) return;
         r.sms[dev] = n;
@@ -116,17 +116,24 @@ int decode(const kv4::Cache& c, kv4::Attend a, void* ws, size_t ws_bytes, Decode
     constexpr int R = 8 * NT, D = NG * kv4::kGroup;
     static Resident res;
     auto* kernel = kv4::decode_kernel<NG, NT, BF16>;
-    constexpr int smem = kv4::decode_smem<NG, NT>();
+    constexpr int smem = kv4::kDecodeSmem<NG, NT>;
     int sms = 0, ctas = 0;
-    if (!resident(res, kernel, kv4::kThreads, smem, &sms, &ctas)) return FA_ERR_CUDA;
+    if (!resident(res, kernel, kv4::kThreads, smem, &sms, &ctas, kv4::kClusterSmem<NG, NT>)) return FA_ERR_CUDA;
     DecodePlan plan;
     const long long items = (static_cast<long long>(c.S) * a.G + R - 1) / R * c.Hkv;
     const long long blocks = (static_cast<long long>(c.max_pages) * c.P + 2 * kv4::kBlock - 1) / kv4::kBlock;
     // items of a call, and blocks of a sequence, are numbered with an int
     if (items * c.B > 0x7fffffffLL || items * blocks > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
     plan.items_most = static_cast<int>(items);
-    const bool whole = blocks <= kv4::kWholeBlocks + 1;
-    const long long most = whole ? items * c.B : (items * c.B * blocks + kv4::kWarps - 1) / kv4::kWarps;
+    // Contexts of at most kWholeBlocks blocks for each CTA of a cluster, where
+    // the clusters take no more than two rounds of the GPU: a cluster an item.
+    // Else the blocks are cut into ranges and a second launch joins the parts.
+    int cluster = 1;
+    while (cluster < kv4::kMaxCluster && blocks > static_cast<long long>(kv4::kWholeBlocks) * cluster + 1) cluster *= 2;
+    const bool whole = blocks <= static_cast<long long>(kv4::kWholeBlocks) * cluster + 1 &&
+                       (cluster == 1 || items * c.B * cluster <= 2LL * sms * ctas);
+    if (whole && items * c.B * cluster > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
+    const long long most = whole ? items * c.B * cluster : (items * c.B * blocks + kv4::kWarps - 1) / kv4::kWarps;
     plan.grid = static_cast<int>(whole ? most : std::min<long long>(most, static_cast<long long>(sms) * ctas));
     const size_t slots = whole ? 0 : static_cast<size_t>(plan.grid) * 2 * R;
     plan.bytes = slots * (D * sizeof(float) + sizeof(float2));
@@ -140,6 +147,21 @@ int decode(const kv4::Cache& c, kv4::Attend a, void* ws, size_t ws_bytes, Decode
     a.part_ml = reinterpret_cast<float2*>(a.part_o + slots * D);
     a.grid = plan.grid;
     a.whole = whole ? plan.items_most : 0;
+    a.cluster = whole ? cluster : 1;
+    if (whole && cluster > 1) {
+        cudaLaunchAttribute dim[1];
+        dim[0].id = cudaLaunchAttributeClusterDimension;
+        dim[0].val.clusterDim.x = static_cast<unsigned>(cluster);
+        dim[0].val.clusterDim.y = dim[0].val.clusterDim.z = 1;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(static_cast<unsigned>(plan.grid));
+        cfg.blockDim = dim3(kv4::kThreads);
+        cfg.dynamicSmemBytes = smem + kv4::kClusterSmem<NG, NT>;
+        cfg.stream = st;
+        cfg.attrs = dim;
+        cfg.numAttrs = 1;
+        return cudaLaunchKernelEx(&cfg, kernel, c, a) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+    }
     kernel<<<plan.grid, kv4::kThreads, smem, st>>>(c, a);
     if (launched() != FA_OK) return FA_ERR_CUDA;
     if (whole) return FA_OK;

@@ -42,8 +42,9 @@
 // (at most two a warp) are joined once, at the end of the CTA.  Sharing each
 // item's blocks out to the warps in turn, with a join for each item, left
 // the warps waiting for one another: batch of 64 ragged contexts, 84 us.
-// Short contexts (all of an item's blocks: kWholeBlocks) are not cut between
-// CTAs: a CTA an item, one launch.
+// Short contexts are not cut like that: an item has a cluster of 1 to 8 CTAs
+// (at most kWholeBlocks blocks each), which join through one another's shared
+// memory: one launch, no workspace, and no search for the range.
 #pragma once
 
 #include "kv4_cache.cuh"
@@ -52,11 +53,11 @@ namespace kv4 {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kStages = 2;
 constexpr int kBlock = 32;              // keys a block
 constexpr float kLazy = 8.f;            // p may reach 2^kLazy before m moves
 constexpr int kHead = 7;                // p s 2^(kHead - E) < 2^(kLazy + kHead) < 65504
-constexpr int kWholeBlocks = 16;        // most blocks of an item that is never cut
+constexpr int kWholeBlocks = 16;        // most blocks a CTA of an item that has a cluster of its own
+constexpr int kMaxCluster = 8;
 constexpr float kNegInf = -INFINITY;
 constexpr uint32_t kMid = 0x00f000f0u;  // bits 4..7 of both halves
 
@@ -72,7 +73,8 @@ struct Attend {
     float* part_o;                       // [2 grid][8 NT][D]
     float2* part_ml;                     // [2 grid][8 NT]: reference and sum
     int grid;                            // CTAs of decode_kernel
-    int whole;                           // nonzero: a CTA an item, of this many items a sequence
+    int whole;                           // nonzero: a cluster an item, of this many items a sequence
+    int cluster;                         // its CTAs
 };
 
 template <int NG>
@@ -81,6 +83,10 @@ struct Tile {
     static constexpr int kCodes = kBlock * 16 * NG;        // bytes of K's (V's) codes in a block
     static constexpr int kScales = kBlock * 2 * NG;
     static constexpr int kStage = 2 * (kCodes + kScales);
+    // As many blocks in flight as leave room for three CTAs an SM (D <= 128; two
+    // above): a block's copies take about 2 us under load, whatever its size, and
+    // with two stages that was the time of a block.
+    static constexpr int kStages = NG <= 2 ? 6 : NG == 3 ? 4 : NG <= 6 ? 3 : 2;
     static constexpr int kRing = kWarps * kStages * kStage;
 };
 
@@ -91,11 +97,12 @@ constexpr int kPartFloats = 8 * NT * (Tile<NG>::D + 4);
 
 // The ring, a part for each warp (the second one, of its last item, goes into
 // its own ring, which is empty by then), the rest.
+// A cluster's CTAs have room for their joined sums besides.
 template <int NG, int NT>
-constexpr int decode_smem() {
-    static_assert(kPartFloats<NG, NT> * 4 <= kStages * Tile<NG>::kStage, "a part fits the ring");
-    return Tile<NG>::kRing + kWarps * kPartFloats<NG, NT> * 4 + 2048;
-}
+constexpr int kClusterSmem = 8 * NT * (Tile<NG>::D * 4 + 8);
+
+template <int NG, int NT>
+constexpr int kDecodeSmem = Tile<NG>::kRing + kWarps * kPartFloats<NG, NT> * 4 + 2048;
 
 // The rows of the call for a sequence as items: tiles x heads, each of `blocks` key blocks from key `first`.
 struct Work {
@@ -215,6 +222,32 @@ __device__ __forceinline__ void copies_wait() {   // all but the last N groups o
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The address of this CTA's shared memory `at` in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t cluster_map(uint32_t at, uint32_t rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(at), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ float2 cluster_load2(uint32_t at) {
+    float2 v;
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(at) : "memory");
+    return v;
+}
+__device__ __forceinline__ float4 cluster_load4(uint32_t at) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at) : "memory");
+    return v;
+}
+
 __device__ __forceinline__ void mma16816(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
     asm volatile(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -247,9 +280,9 @@ __device__ __forceinline__ uint32_t high_codes(uint32_t u) {
     return half_sub((u & kMid) | 0x64006400u, 0x64806480u);
 }
 
-// Where warp `warp` starts among its CTA's blocks.
-__device__ __forceinline__ int share(int blocks, int warp) {
-    return static_cast<int>(static_cast<long long>(blocks) * warp / kWarps);
+// Where share `i` of n starts among some blocks.
+__device__ __forceinline__ int share(int blocks, int i, int n) {
+    return static_cast<int>(static_cast<long long>(blocks) * i / n);
 }
 
 // A warp's copies: the blocks of its range one after the other, each in runs of
@@ -273,7 +306,8 @@ struct Copier {
         const int key0 = cur.w.first + cur.blk * kBlock;
         const int* row = c.table + static_cast<long long>(cur.b) * c.max_pages;
         if (key0 < cur.w.len) page[0] = __ldg(row + pg);
-        if (key0 + 16 < cur.w.len) page[1] = off + 16 < c.P ? page[0] : __ldg(row + pg + 1);
+        // (looking at page[0] here would wait for it)
+        if (key0 + 16 < cur.w.len && off + 16 >= c.P) page[1] = __ldg(row + pg + 1);
     }
     // The place of the block at `cur`, from scratch.
     __device__ __forceinline__ void locate(const Cache& c) {
@@ -291,7 +325,8 @@ struct Copier {
             const int key0 = cur.w.first + cur.blk * kBlock;
             const bool ask0 = key0 < cur.w.len, ask1 = key0 + 16 < cur.w.len;
             const bool ok0 = ask0 && static_cast<unsigned>(page[0]) < static_cast<unsigned>(c.pages);
-            const bool ok1 = ask1 && static_cast<unsigned>(page[1]) < static_cast<unsigned>(c.pages);
+            const int page1 = off + 16 < c.P ? page[0] : page[1];
+            const bool ok1 = ask1 && static_cast<unsigned>(page1) < static_cast<unsigned>(c.pages);
             if (ask0 != ok0 || ask1 != ok1) report(kStatusBadPages);
             in = (ok0 ? 1u : 0u) | (ok1 ? 2u : 0u);
             const uint32_t dst = fa::ptx::smem_addr(st) + lane * 16;
@@ -316,7 +351,7 @@ struct Copier {
                 }
             } else if (in != 0) {
                 const int off1 = off + 16 < c.P ? off + 16 : 0;
-                const long long row1 = (static_cast<long long>(ok1 ? page[1] : 0) * 2 * c.Hkv + head) * c.P + off1;
+                const long long row1 = (static_cast<long long>(ok1 ? page1 : 0) * 2 * c.Hkv + head) * c.P + off1;
 #pragma unroll 1
                 for (int i = 0; i < NG; ++i) {
                     const int q = i * 32 + lane;
@@ -378,7 +413,8 @@ __device__ __forceinline__ void write_row(const Cache& c, const Attend& a, const
 
 template <int NG, int NT, bool BF16>
 __global__ void __launch_bounds__(kThreads, NG <= 4 && NT == 1 ? 3 : 2) decode_kernel(Cache c, Attend a) {
-    constexpr int D = NG * kGroup, R = 8 * NT, kStage = Tile<NG>::kStage;
+    constexpr int D = NG * kGroup, R = 8 * NT, kStage = Tile<NG>::kStage, kStages = Tile<NG>::kStages;
+    static_assert(kPartFloats<NG, NT> * 4 <= kStages * kStage, "a part fits the ring");
     constexpr int kPart = kPartFloats<NG, NT>;
     extern __shared__ __align__(128) uint8_t smem[];
     uint8_t* ring = smem;
@@ -394,12 +430,13 @@ __global__ void __launch_bounds__(kThreads, NG <= 4 && NT == 1 ? 3 : 2) decode_k
     Cursor seg;
     int blocks;
     if (a.whole) {
-        seg.b = blockIdx.x / a.whole;
-        seg.item = blockIdx.x - seg.b * a.whole;
-        seg.blk = 0;
-        seg.w = work_of(c, a, seg.b, R, tid == 0 && seg.item == 0);
-        if (seg.item >= seg.w.items) return;
-        blocks = seg.w.blocks;
+        const int x = blockIdx.x / a.cluster, rank = blockIdx.x - x * a.cluster;
+        seg.b = x / a.whole;
+        seg.item = x - seg.b * a.whole;
+        seg.w = work_of(c, a, seg.b, R, tid == 0 && seg.item == 0 && rank == 0);
+        if (seg.item >= seg.w.items) return;   // the whole cluster
+        seg.blk = share(seg.w.blocks, rank, a.cluster);
+        blocks = share(seg.w.blocks, rank + 1, a.cluster) - seg.blk;
     } else {
         const Range range = find_range(c, a, R, scan);
         fa::ptx::launch_dependents();
@@ -413,8 +450,8 @@ __global__ void __launch_bounds__(kThreads, NG <= 4 && NT == 1 ? 3 : 2) decode_k
         seg.blk = off - seg.item * seg.w.blocks;
     }
     uint8_t* my_ring = ring + warp * kStages * kStage;
-    int x = share(blocks, warp);                            // this warp's next block
-    const int x_end = share(blocks, warp + 1);
+    int x = share(blocks, warp, kWarps);                    // this warp's next block
+    const int x_end = share(blocks, warp + 1, kWarps);
     if (lane < 2) parts[warp * 2 + lane].b = -1;
     __syncwarp();
     seg.blk += x;
@@ -733,7 +770,7 @@ __global__ void __launch_bounds__(kThreads, NG <= 4 && NT == 1 ? 3 : 2) decode_k
 
         // ---- the item's end: its result, or a part to be joined.  Sums are in
         // units of 2^(m - kHead + E).
-        const bool whole = seg.blk == 0 && seg_blocks == w.blocks;
+        const bool whole = seg.blk == 0 && seg_blocks == w.blocks && a.cluster <= 1;
         const int part = seg.blk == 0 ? 1 : 0;
         float* dst = part == 0 ? join + warp * kPart : reinterpret_cast<float*>(ring + warp * kStages * kStage);
 #pragma unroll
@@ -774,6 +811,68 @@ __global__ void __launch_bounds__(kThreads, NG <= 4 && NT == 1 ? 3 : 2) decode_k
     // that starts and ends its item is the result, else it goes to the
     // CTA's slot 0 (carries an item on) or 1 (starts one).
     __syncthreads();
+    if (a.whole && a.cluster > 1) {
+        // all parts are of the cluster's item: join them here, then over the cluster
+        float* sums = reinterpret_cast<float*>(smem + kDecodeSmem<NG, NT>);
+        float2* mls = reinterpret_cast<float2*>(sums + R * D);
+        const Work w = work_of(c, a, seg.b, R, false);
+        const int item = (blockIdx.x / a.cluster) % a.whole;
+        const int head = item / w.tiles, tile = item - head * w.tiles;
+        const int rows = min(R, w.n * a.G - tile * R);
+        for (int i = tid; i < rows * (D / 4); i += kThreads) {
+            const int rr = i / (D / 4), d4 = i - rr * (D / 4);
+            float m = kNegInf, l = 0.f;
+#pragma unroll
+            for (int k = 0; k < 2 * kWarps; ++k)
+                if (parts[k].b >= 0) m = fmaxf(m, join_ml[k * R + rr].x);
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int k = 0; k < 2 * kWarps; ++k) {
+                if (parts[k].b < 0) continue;
+                const float2 ml = join_ml[k * R + rr];
+                const float f = ml.x == kNegInf ? 0.f : fa::ptx::ex2_approx(ml.x - m);
+                const float* src = (k & 1) ? reinterpret_cast<const float*>(ring + (k >> 1) * kStages * kStage)
+                                           : join + (k >> 1) * kPart;
+                const float4 v = *reinterpret_cast<const float4*>(src + rr * (D + 4) + 4 * d4);
+                l += f * ml.y;
+                o.x += f * v.x;
+                o.y += f * v.y;
+                o.z += f * v.z;
+                o.w += f * v.w;
+            }
+            *reinterpret_cast<float4*>(sums + rr * D + 4 * d4) = o;
+            if (d4 == 0) mls[rr] = make_float2(m, l);
+        }
+        cluster_sync();
+        const uint32_t sums_at = fa::ptx::smem_addr(sums), mls_at = fa::ptx::smem_addr(mls);
+        for (int i = cluster_rank() * kThreads + tid; i < rows * (D / 4); i += a.cluster * kThreads) {
+            const int rr = i / (D / 4), d4 = i - rr * (D / 4);
+            float2 ml[kMaxCluster];
+            float4 v[kMaxCluster];
+            float m = kNegInf, l = 0.f;
+#pragma unroll
+            for (int k = 0; k < kMaxCluster; ++k) {
+                if (k >= a.cluster) continue;
+                ml[k] = cluster_load2(cluster_map(mls_at + rr * 8, k));
+                v[k] = cluster_load4(cluster_map(sums_at + (rr * D + 4 * d4) * 4, k));
+                m = fmaxf(m, ml[k].x);
+            }
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int k = 0; k < kMaxCluster; ++k) {
+                if (k >= a.cluster) continue;
+                const float f = ml[k].x == kNegInf ? 0.f : fa::ptx::ex2_approx(ml[k].x - m);
+                l += f * ml[k].y;
+                o.x += f * v[k].x;
+                o.y += f * v[k].y;
+                o.z += f * v[k].z;
+                o.w += f * v[k].w;
+            }
+            write_row<BF16>(c, a, w, seg.b, D, tile * R + rr, head, 4 * d4, o, m, l, d4 == 0 && a.lse != nullptr);
+        }
+        cluster_sync();   // no CTA's shared memory goes before the others have read it
+        return;
+    }
     for (int p = 0; p < 2 * kWarps;) {
         const Part first = parts[p];
         if (first.b < 0) {
