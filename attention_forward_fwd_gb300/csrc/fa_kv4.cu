@@ -71,9 +71,10 @@ bool bad_strides(const long long* s, int unit) {
     return s[0] % unit != 0 || s[1] % unit != 0 || s[2] % unit != 0;
 }
 
-// Blocks of a launch over rows (8 threads a row, K and V of every head); 0: too many.
+// Blocks of a launch over the call's rows, K and V of every head; 0: too many.
+template <int NG>
 unsigned row_blocks(const kv4::Cache& c) {
-    const long long warps = (static_cast<long long>(c.total) + 3) / 4 * 2 * c.Hkv;
+    const long long warps = (static_cast<long long>(c.total) + 3) / 4 * ((2LL * c.Hkv + kv4::kRows<NG> - 1) / kv4::kRows<NG>);
     const long long blocks = (warps + kv4::kRowThreads / 32 - 1) / (kv4::kRowThreads / 32);
     return blocks > 0x7fffffffLL ? 0u : static_cast<unsigned>(blocks);
 }
@@ -279,6 +280,30 @@ int decode_any(int D, bool bf16, const kv4::Cache& c, const kv4::Attend& a, void
 #undef KV4_TWO
 }
 
+template <int NG>
+int write(const kv4::Cache& c, const kv4::RowIo& io, bool bf16, cudaStream_t st) {
+    const unsigned blocks = row_blocks<NG>(c);
+    if (blocks == 0) return FA_ERR_UNSUPPORTED;
+    const bool values = io.k_out != nullptr;
+    if (bf16) {
+        if (values) kv4::write_kernel<NG, true, true><<<blocks, kv4::kRowThreads, 0, st>>>(c, io);
+        else kv4::write_kernel<NG, true, false><<<blocks, kv4::kRowThreads, 0, st>>>(c, io);
+    } else {
+        if (values) kv4::write_kernel<NG, false, true><<<blocks, kv4::kRowThreads, 0, st>>>(c, io);
+        else kv4::write_kernel<NG, false, false><<<blocks, kv4::kRowThreads, 0, st>>>(c, io);
+    }
+    return launched();
+}
+
+template <int NG>
+int read(const kv4::Cache& c, const kv4::RowIo& io, bool bf16, cudaStream_t st) {
+    const unsigned blocks = row_blocks<NG>(c);
+    if (blocks == 0) return FA_ERR_UNSUPPORTED;
+    if (bf16) kv4::read_kernel<NG, true><<<blocks, kv4::kRowThreads, 0, st>>>(c, io);
+    else kv4::read_kernel<NG, false><<<blocks, kv4::kRowThreads, 0, st>>>(c, io);
+    return launched();
+}
+
 template <int VEC, bool INTER>
 int rotate(const rot::Rotary& p, bool bf16, unsigned blocks, size_t smem, cudaStream_t st) {
     if (bf16) rot::rotary_kernel<VEC, INTER, true><<<blocks, rot::kThreads, smem, st>>>(p);
@@ -301,16 +326,9 @@ int fa_kv4_write(const fa_kv4_cache_t* cache, const void* K, const void* V, cons
     if (misaligned(K, 8) || misaligned(V, 8) || misaligned(K_out, 8) || misaligned(V_out, 8) ||
         bad_strides(k_strides, 4) || bad_strides(v_strides, 4))
         return FA_ERR_UNSUPPORTED;
-    const unsigned blocks = row_blocks(c);
-    if (blocks == 0) return FA_ERR_UNSUPPORTED;
     const kv4::RowIo io = {K, V, k_strides[0], k_strides[1], k_strides[2], v_strides[0], v_strides[1],
                            v_strides[2], K_out, V_out};
-    const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-#define KV4_ONE(NG_)                                                                            \
-    case NG_:                                                                                   \
-        if (dtype == FA_BF16) kv4::write_kernel<NG_, true><<<blocks, kv4::kRowThreads, 0, st>>>(c, io); \
-        else kv4::write_kernel<NG_, false><<<blocks, kv4::kRowThreads, 0, st>>>(c, io);         \
-        return launched()
+#define KV4_ONE(NG_) case NG_: return write<NG_>(c, io, dtype == FA_BF16, reinterpret_cast<cudaStream_t>(stream))
     switch (cache->D / kv4::kGroup) {
         KV4_ONE(1); KV4_ONE(2); KV4_ONE(3); KV4_ONE(4); KV4_ONE(5); KV4_ONE(6); KV4_ONE(7); KV4_ONE(8);
         default: return FA_ERR_UNSUPPORTED;
@@ -324,17 +342,10 @@ int fa_kv4_read(const fa_kv4_cache_t* cache, void* K, void* V, int dtype, fa_str
     if (v != FA_OK) return v;
     if (K == nullptr || V == nullptr) return FA_ERR_INVALID_ARG;
     if (misaligned(K, 16) || misaligned(V, 16)) return FA_ERR_UNSUPPORTED;
-    const unsigned blocks = row_blocks(c);
-    if (blocks == 0) return FA_ERR_UNSUPPORTED;
     kv4::RowIo io = {};
     io.k_out = K;
     io.v_out = V;
-    const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-#define KV4_ONE(NG_)                                                                            \
-    case NG_:                                                                                   \
-        if (dtype == FA_BF16) kv4::read_kernel<NG_, true><<<blocks, kv4::kRowThreads, 0, st>>>(c, io); \
-        else kv4::read_kernel<NG_, false><<<blocks, kv4::kRowThreads, 0, st>>>(c, io);          \
-        return launched()
+#define KV4_ONE(NG_) case NG_: return read<NG_>(c, io, dtype == FA_BF16, reinterpret_cast<cudaStream_t>(stream))
     switch (cache->D / kv4::kGroup) {
         KV4_ONE(1); KV4_ONE(2); KV4_ONE(3); KV4_ONE(4); KV4_ONE(5); KV4_ONE(6); KV4_ONE(7); KV4_ONE(8);
         default: return FA_ERR_UNSUPPORTED;

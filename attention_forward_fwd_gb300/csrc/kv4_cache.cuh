@@ -230,149 +230,226 @@ struct RowIo {
     void* v_out;
 };
 
-constexpr int kRowThreads = 256;   // 32 rows a block, 8 threads a row
+// Both kernels: a warp takes four tokens, 8 neighbouring threads each, and
+// kRows<NG> of their rows (K or V of a head) one after the other: where a token
+// lies is found once for all of them, while the first rows' loads are under
+// way.  Thread r of a row holds elements 4 r .. 4 r + 3 of every group: 8-byte
+// accesses to the 16-bit tensor, 64 contiguous bytes a group, and 2 NG
+// contiguous bytes of codes.  The four rows of an access are four tokens of the
+// same head, so that their scales fill whole sectors.
+constexpr int kRowThreads = 256;
+template <int NG>
+constexpr int kRows = NG <= 2 ? 8 : NG <= 4 ? 4 : 2;
 
-// One row by 8 neighbouring threads: thread r holds elements 4 r .. 4 r + 3 of
-// every group (8-byte loads, 64 contiguous bytes a group), the groups' extremes
-// meet in three shuffles, and the thread's 2 NG bytes of codes leave in one
-// store.  The four rows of a warp are four tokens of the same head, so that
-// their scales fill whole sectors.
-//
+// Which rows a warp takes.
+struct RowShare {
+    int t, first, n;      // token, first row (K's heads, then V's), rows
+};
+template <int NG>
+__device__ __forceinline__ bool row_share(const Cache& c, RowShare* s) {
+    const int rows = 2 * c.Hkv, chunks = (rows + kRows<NG> - 1) / kRows<NG>;
+    const long long w = static_cast<long long>(blockIdx.x) * (kRowThreads / 32) + (threadIdx.x >> 5);
+    const long long t4 = w / chunks;
+    if (t4 >= (static_cast<long long>(c.total) + 3) / 4) return false;
+    s->first = static_cast<int>(w - t4 * chunks) * kRows<NG>;
+    s->n = min(kRows<NG>, rows - s->first);
+    s->t = static_cast<int>(t4) * 4 + ((threadIdx.x >> 3) & 3);
+    return true;
+}
+
+template <bool BF16>
+__device__ __forceinline__ uint32_t max16x2(uint32_t a, uint32_t b) {   // a NaN wins
+    uint32_t r;
+    if constexpr (BF16) asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    else asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// A group's scale from its elements x (this thread's four), the same in the
+// group's 8 threads.
+template <bool BF16>
+__device__ __forceinline__ uint32_t group_scale(uint2 x, int sub) {
+    constexpr uint32_t kInf = BF16 ? 0x7f80u : 0x7c00u;
+    // the largest x in the low half, the largest -x in the high half
+    const uint32_t up = max16x2<BF16>(x.x, x.y), down = max16x2<BF16>(x.x ^ 0x80008000u, x.y ^ 0x80008000u);
+    uint32_t m = max16x2<BF16>(__byte_perm(up, down, 0x5410), __byte_perm(up, down, 0x7632));
+#pragma unroll
+    for (int i = 1; i < 8; i <<= 1) m = max16x2<BF16>(m, __shfl_xor_sync(0xffffffffu, m, i));
+    const float2 top = to_f32x2<BF16>(m);
+    bool positive = top.x > top.y;
+    const bool tie = top.x == top.y && top.x != 0.f;
+    if (__any_sync(0xffffffffu, tie)) {
+        // both signs at the largest magnitude: the first of them counts
+        const uint32_t e[4] = {x.x & 0xffffu, x.x >> 16, x.y & 0xffffu, x.y >> 16};
+        uint32_t key = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            key = max(key, ((e[j] & 0x7fffu) << 16) | ((31u - (sub * 4 + j)) << 1) | (e[j] >> 15));
+#pragma unroll
+        for (int i = 1; i < 8; i <<= 1) key = max(key, __shfl_xor_sync(0xffffffffu, key, i));
+        if (tie) positive = (key & 1u) == 0;
+    }
+    const bool finite = (m & 0x7fffu) < kInf && ((m >> 16) & 0x7fffu) < kInf;
+    const float xe = positive ? top.x : -top.y;
+    const uint32_t sb = pack16<true>(xe * -0.125f, 0.f) & 0xffffu;
+    return !finite ? 0x7fc0u : (sb & 0x7fffu) == 0 ? 0u : sb;
+}
+
+// ------------------------------------------------------------------- write
 // Exactness: rint(x / s) is taken of x * (1 / s), which is off by less than
 // 2^-21.  x has at most 11 significant bits and s at most 8, so x / s is
 // either a tie k + 1/2 or at least 2^-13 away from one; rounding the product
 // to multiples of 2^-14 first restores the ties and moves nothing across one.
-template <int NG, bool BF16>
+template <int NG, bool BF16, bool VALUES>
 __global__ void __launch_bounds__(kRowThreads) write_kernel(Cache c, RowIo io) {
-    constexpr int D = NG * kGroup;
+    constexpr int D = NG * kGroup, N = kRows<NG>;
     if (blockIdx.x == 0) check_sequences(c);
+    RowShare own;
+    if (!row_share<NG>(c, &own)) return;
     const int sub = threadIdx.x & 7;                       // r
-    const int tokens4 = (c.total + 3) >> 2;
-    const long long warps = static_cast<long long>(tokens4) * 2 * c.Hkv;
-    const long long w = static_cast<long long>(blockIdx.x) * (kRowThreads / 32) + (threadIdx.x >> 5);
-    if (w >= warps) return;
-    const int head = static_cast<int>(w % c.Hkv);
-    const long long w2 = w / c.Hkv;
-    const int which = static_cast<int>(w2 & 1);
-    const int t = static_cast<int>(w2 >> 1) * 4 + ((threadIdx.x >> 3) & 3);
+    uint2 x[N][NG];
+    {
+        const bool here = own.t < c.total;
+        const long long batch = c.cu != nullptr || !here ? 0 : own.t / c.S, row = here ? own.t - batch * c.S : 0;
+        const uint16_t* k = static_cast<const uint16_t*>(io.k) + batch * io.k_batch + row * io.k_row + sub * 4;
+        const uint16_t* v = static_cast<const uint16_t*>(io.v) + batch * io.v_batch + row * io.v_row + sub * 4;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int y = own.first + i;
+            const uint16_t* src = y < c.Hkv ? k + y * io.k_head : v + (y - c.Hkv) * io.v_head;
+#pragma unroll
+            for (int g = 0; g < NG; ++g)
+                x[i][g] = i < own.n && here ? *reinterpret_cast<const uint2*>(src + g * kGroup) : make_uint2(0, 0);
+        }
+    }
     long long page = 0;
     int at = 0;
-    RowPlace place = kRowSkip;
-    uint2 x[NG];
-    if (t < c.total) {
-        const long long batch = c.cu != nullptr ? 0 : t / c.S, row = c.cu != nullptr ? t : t - batch * c.S;
-        const uint16_t* src = which == 0
-            ? static_cast<const uint16_t*>(io.k) + batch * io.k_batch + row * io.k_row + head * io.k_head
-            : static_cast<const uint16_t*>(io.v) + batch * io.v_batch + row * io.v_row + head * io.v_head;
+    const RowPlace place = own.t < c.total ? place_of(c, own.t, &page, &at) : kRowSkip;
 #pragma unroll
-        for (int g = 0; g < NG; ++g) x[g] = *reinterpret_cast<const uint2*>(src + g * kGroup + sub * 4);
-        place = place_of(c, t, &page, &at);
-    } else {
+    for (int i = 0; i < N; ++i) {
+        if (i >= own.n) break;
+        const int y = own.first + i, which = y >= c.Hkv ? 1 : 0, head = y - which * c.Hkv;
+        Words<NG> codes, scales;
+        codes.clear();
+        scales.clear();
+        uint2 out[NG];
 #pragma unroll
-        for (int g = 0; g < NG; ++g) x[g] = make_uint2(0, 0);
-    }
-    constexpr uint32_t kInf = BF16 ? 0x7f80u : 0x7c00u;
-    Words<NG> codes, scales;
-    codes.clear();
-    scales.clear();
-    uint2 y[NG];
+        for (int g = 0; g < NG; ++g) {
+            const uint32_t sb = group_scale<BF16>(x[i][g], sub);
+            const float s = bf16_bits(sb);
+            const bool some = sb != 0 && sb != 0x7fc0u;
+            // scales below 2^-64 are lifted by 2^96 (exactly) so that 1 / s is finite
+            const float lift = fabsf(s) < 5.42101086e-20f ? 7.92281625e28f : 1.f;
+            const float inv = some ? __frcp_rn(s * lift) : 0.f;
+            const float2 a = to_f32x2<BF16>(x[i][g].x), b = to_f32x2<BF16>(x[i][g].y);
+            const float e[4] = {a.x, a.y, b.x, b.y};
+            uint32_t word = 0;
+            float q[4];
 #pragma unroll
-    for (int g = 0; g < NG; ++g) {
-        // (magnitude, first of equals, sign) in one word whose maximum is x_e
-        const uint32_t e[4] = {x[g].x & 0xffffu, x[g].x >> 16, x[g].y & 0xffffu, x[g].y >> 16};
-        uint32_t key = 0;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const uint32_t kj = ((e[j] & 0x7fffu) << 16) | ((31u - (sub * 4 + j)) << 1) | (e[j] >> 15);
-            key = max(key, kj);
+            for (int j = 0; j < 4; ++j) {
+                float u = some ? (e[j] * lift) * inv : 0.f;
+                u = __fadd_rn(__fadd_rn(u, 768.f), -768.f);            // to multiples of 2^-14
+                u = fminf(fmaxf(u, -8.f), 7.f);
+                const float m = __fadd_rn(u, 12582920.f);              // 8 more than the nearest integer, ties to even
+                word |= (__float_as_uint(m) & 15u) << (4 * j);
+                if constexpr (VALUES) q[j] = __fadd_rn(m, -12582920.f) * s;
+            }
+            codes.set(g, word);
+            scales.set(g, sb);
+            if constexpr (VALUES) out[g] = make_uint2(pack16<BF16>(q[0], q[1]), pack16<BF16>(q[2], q[3]));
         }
-#pragma unroll
-        for (int m = 1; m < 8; m <<= 1) key = max(key, __shfl_xor_sync(0xffffffffu, key, m));
-        const uint32_t mag = key >> 16;
-        const float xe = to_f32x2<BF16>(mag | ((key & 1u) << 15)).x;
-        uint32_t sb = pack16<true>(xe * -0.125f, 0.f) & 0xffffu;
-        const bool finite = mag < kInf, some = finite && (sb & 0x7fffu) != 0;
-        if (!some) sb = finite ? 0u : 0x7fc0u;
-        const float s = bf16_bits(sb);
-        // scales below 2^-64 are lifted by 2^96 (exactly) so that 1 / s is finite
-        const float lift = fabsf(s) < 5.42101086e-20f ? 7.92281625e28f : 1.f;
-        const float inv = some ? __frcp_rn(s * lift) : 0.f;
-        const float2 a = to_f32x2<BF16>(x[g].x), b = to_f32x2<BF16>(x[g].y);
-        const float v[4] = {a.x, a.y, b.x, b.y};
-        uint32_t word = 0;
-        float q[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            float u = some ? (v[j] * lift) * inv : 0.f;
-            u = __fadd_rn(__fadd_rn(u, 768.f), -768.f);            // to multiples of 2^-14
-            u = fminf(fmaxf(u, -8.f), 7.f);
-            const float m = __fadd_rn(u, 12582912.f);              // to the nearest integer, ties to even
-            word |= ((__float_as_uint(m) + 8u) & 15u) << (4 * j);
-            q[j] = __fadd_rn(m, -12582912.f) * s;
+        if (place == kRowOk) {
+            const long long row = ((page * 2 + which) * c.Hkv + head) * c.P + at;
+            codes.store(c.codes + row * (16 * NG) + sub * (2 * NG));
+            if (sub == 0) scales.store(c.scales + row * NG);
         }
-        codes.set(g, word);
-        scales.set(g, sb);
-        y[g] = make_uint2(pack16<BF16>(q[0], q[1]), pack16<BF16>(q[2], q[3]));
-    }
-    if (place == kRowOk) {
-        const long long row = ((page * 2 + which) * c.Hkv + head) * c.P + at;
-        codes.store(c.codes + row * (16 * NG) + sub * (2 * NG));
-        if (sub == 0) scales.store(c.scales + row * NG);
-    }
-    void* out = which == 0 ? io.k_out : io.v_out;
-    if (out != nullptr && place != kRowSkip) {
-        uint16_t* dst = static_cast<uint16_t*>(out) + (static_cast<long long>(t) * c.Hkv + head) * D;
+        if constexpr (VALUES) {
+            if (place != kRowSkip) {
+                uint16_t* dst = static_cast<uint16_t*>(which == 0 ? io.k_out : io.v_out) +
+                                (static_cast<long long>(own.t) * c.Hkv + head) * D;
 #pragma unroll
-        for (int g = 0; g < NG; ++g)
-            *reinterpret_cast<uint2*>(dst + g * kGroup + sub * 4) = place == kRowOk ? y[g] : make_uint2(0, 0);
+                for (int g = 0; g < NG; ++g)
+                    *reinterpret_cast<uint2*>(dst + g * kGroup + sub * 4) = place == kRowOk ? out[g] : make_uint2(0, 0);
+            }
+        }
     }
 }
 
 // -------------------------------------------------------------------- read
-// The same shape backwards: 8 threads a row, 2 NG bytes of codes in and NG
-// times 8 bytes out each.  A row before the sequence's first token is zeros;
-// a row that is skipped stays as it was.
+// The same shape backwards.  Two codes at a time become n - 8 in the result's
+// own type, 2^k + n (k = 7 in bf16, 10 in fp16) less 2^k + 8, and are multiplied by
+// the scale there: in bf16 that is the one rounding; in fp16 it is exact, or the
+// one rounding to a subnormal, while the scale is a normal fp16 (others
+// go through fp32).  A row before the sequence's first token is zeros; a row that is
+// skipped stays as it was.
+template <bool BF16>
+__device__ __forceinline__ uint32_t code_values(uint32_t pair, uint32_t s2) {
+    const uint32_t y = (pair & 0x000f000fu) | (BF16 ? 0x43004300u : 0x64006400u);
+    uint32_t r;
+    if constexpr (BF16) {
+        asm("{\n\t.reg .b32 t;\n\tsub.rn.bf16x2 t, %1, %2;\n\tmul.rn.bf16x2 %0, t, %3;\n\t}"
+            : "=r"(r) : "r"(y), "r"(0x43084308u), "r"(s2));
+    } else {
+        asm("{\n\t.reg .b32 t;\n\tsub.rn.f16x2 t, %1, %2;\n\tmul.rn.f16x2 %0, t, %3;\n\t}"
+            : "=r"(r) : "r"(y), "r"(0x64086408u), "r"(s2));
+    }
+    return r;
+}
+
 template <int NG, bool BF16>
 __global__ void __launch_bounds__(kRowThreads) read_kernel(Cache c, RowIo io) {
-    constexpr int D = NG * kGroup;
+    constexpr int D = NG * kGroup, N = kRows<NG>;
     if (blockIdx.x == 0) check_sequences(c);
+    RowShare own;
+    if (!row_share<NG>(c, &own) || own.t >= c.total) return;
     const int sub = threadIdx.x & 7;
-    const int tokens4 = (c.total + 3) >> 2;
-    const long long warps = static_cast<long long>(tokens4) * 2 * c.Hkv;
-    const long long w = static_cast<long long>(blockIdx.x) * (kRowThreads / 32) + (threadIdx.x >> 5);
-    if (w >= warps) return;
-    const int head = static_cast<int>(w % c.Hkv);
-    const long long w2 = w / c.Hkv;
-    const int which = static_cast<int>(w2 & 1);
-    const int t = static_cast<int>(w2 >> 1) * 4 + ((threadIdx.x >> 3) & 3);
-    if (t >= c.total) return;
     long long page = 0;
     int at = 0;
-    const RowPlace place = place_of(c, t, &page, &at);
+    const RowPlace place = place_of(c, own.t, &page, &at);
     if (place == kRowSkip) return;
-    Words<NG> codes, scales;
-    if (place == kRowOk) {
-        const long long row = ((page * 2 + which) * c.Hkv + head) * c.P + at;
-        codes.load(c.codes + row * (16 * NG) + sub * (2 * NG));
-        scales.load(c.scales + row * NG);
-    } else {
-        codes.clear();
-        scales.clear();
-    }
-    uint16_t* dst = static_cast<uint16_t*>(which == 0 ? io.k_out : io.v_out) +
-                    (static_cast<long long>(t) * c.Hkv + head) * D;
+    Words<NG> codes[N], scales[N];
 #pragma unroll
-    for (int g = 0; g < NG; ++g) {
-        const float s = scales.bf16(g);
-        const uint32_t word = codes.get(g);
-        float q[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int n = static_cast<int>((word >> (4 * j)) & 15u) - 8;
-            q[j] = place == kRowOk ? static_cast<float>(n) * s : 0.f;
+    for (int i = 0; i < N; ++i) {
+        codes[i].clear();
+        scales[i].clear();
+        if (i < own.n && place == kRowOk) {
+            const int y = own.first + i;   // K's heads, then V's: as they lie in the page
+            const long long row = (page * 2 * c.Hkv + y) * c.P + at;
+            codes[i].load_global(c.codes + row * (16 * NG) + sub * (2 * NG));
+            scales[i].load_global(c.scales + row * NG);
         }
-        *reinterpret_cast<uint2*>(dst + g * kGroup + sub * 4) =
-            make_uint2(pack16<BF16>(q[0], q[1]), pack16<BF16>(q[2], q[3]));
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        if (i >= own.n) break;
+        const int y = own.first + i, which = y >= c.Hkv ? 1 : 0, head = y - which * c.Hkv;
+        uint16_t* dst = static_cast<uint16_t*>(which == 0 ? io.k_out : io.v_out) +
+                        (static_cast<long long>(own.t) * c.Hkv + head) * D + sub * 4;
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+            const uint32_t w = codes[i].get(g), t = w | (w << 12);
+            uint2 out;
+            const uint32_t sb = scales[i].get(g);
+            bool plain = true;
+            uint32_t s2 = sb | (sb << 16);
+            if constexpr (!BF16) {
+                const float s = bf16_bits(sb);
+                s2 = pack16<false>(s, s);
+                const uint32_t mag = sb & 0x7fffu;
+                plain = mag == 0 || (mag >= 0x3880u && mag < 0x4780u);     // 2^-14 <= |s| < 2^16
+            }
+            if (plain) {
+                out = make_uint2(code_values<BF16>(t, s2), code_values<BF16>(t >> 8, s2));
+            } else {
+                const float s = bf16_bits(sb);
+                float q[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) q[j] = static_cast<float>(static_cast<int>((w >> (4 * j)) & 15u) - 8) * s;
+                out = make_uint2(pack16<BF16>(q[0], q[1]), pack16<BF16>(q[2], q[3]));
+            }
+            if (place != kRowOk) out = make_uint2(0, 0);
+            *reinterpret_cast<uint2*>(dst + g * kGroup) = out;
+        }
     }
 }
 
