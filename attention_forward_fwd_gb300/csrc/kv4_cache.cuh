@@ -265,111 +265,136 @@ __device__ __forceinline__ uint32_t max16x2(uint32_t a, uint32_t b) {   // a NaN
     return r;
 }
 
-// A group's scale from its elements x (this thread's four), the same in the
-// group's 8 threads.
+template <bool BF16>
+__device__ __forceinline__ uint32_t min16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    if constexpr (BF16) asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    else asm("min.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// A group's scale (its bits) from its elements x (this thread's four), the
+// same in the group's 8 threads.
 template <bool BF16>
 __device__ __forceinline__ uint32_t group_scale(uint2 x, int sub) {
-    constexpr uint32_t kInf = BF16 ? 0x7f80u : 0x7c00u;
     // the largest x in the low half, the largest -x in the high half
-    const uint32_t up = max16x2<BF16>(x.x, x.y), down = max16x2<BF16>(x.x ^ 0x80008000u, x.y ^ 0x80008000u);
+    const uint32_t up = max16x2<BF16>(x.x, x.y), down = min16x2<BF16>(x.x, x.y) ^ 0x80008000u;
     uint32_t m = max16x2<BF16>(__byte_perm(up, down, 0x5410), __byte_perm(up, down, 0x7632));
 #pragma unroll
     for (int i = 1; i < 8; i <<= 1) m = max16x2<BF16>(m, __shfl_xor_sync(0xffffffffu, m, i));
     const float2 top = to_f32x2<BF16>(m);
-    bool positive = top.x > top.y;
+    float xe = top.x > top.y ? top.x : -top.y;   // NaN if there is one
     const bool tie = top.x == top.y && top.x != 0.f;
     if (__any_sync(0xffffffffu, tie)) {
         // both signs at the largest magnitude: the first of them counts
         const uint32_t e[4] = {x.x & 0xffffu, x.x >> 16, x.y & 0xffffu, x.y >> 16};
         uint32_t key = 0;
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            key = max(key, ((e[j] & 0x7fffu) << 16) | ((31u - (sub * 4 + j)) << 1) | (e[j] >> 15));
-#pragma unroll
+#pragma unroll 1
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t v = j == 0 ? e[0] : j == 1 ? e[1] : j == 2 ? e[2] : e[3];
+            key = max(key, ((v & 0x7fffu) << 16) | ((31u - (sub * 4 + j)) << 1) | (v >> 15));
+        }
+#pragma unroll 1
         for (int i = 1; i < 8; i <<= 1) key = max(key, __shfl_xor_sync(0xffffffffu, key, i));
-        if (tie) positive = (key & 1u) == 0;
+        if (tie && (key & 1u) == 0) xe = top.x;
     }
-    const bool finite = (m & 0x7fffu) < kInf && ((m >> 16) & 0x7fffu) < kInf;
-    const float xe = positive ? top.x : -top.y;
     const uint32_t sb = pack16<true>(xe * -0.125f, 0.f) & 0xffffu;
-    return !finite ? 0x7fc0u : (sb & 0x7fffu) == 0 ? 0u : sb;
+    return (sb & 0x7fffu) >= 0x7f80u ? 0x7fc0u : (sb & 0x7fffu) == 0 ? 0u : sb;
 }
 
 // ------------------------------------------------------------------- write
-// Exactness: rint(x / s) is taken of x * (1 / s), which is off by less than
-// 2^-21.  x has at most 11 significant bits and s at most 8, so x / s is
+// Exactness: rint(x / s) is taken of x times an approximate 1 / s, which is off
+// by less than 2^-20.  x has at most 11 significant bits and s at most 8, so x / s is
 // either a tie k + 1/2 or at least 2^-13 away from one; rounding the product
 // to multiples of 2^-14 first restores the ties and moves nothing across one.
+// x / s is at least -8 (1 + 2^-8), which rounds to -8: only 7 needs a clamp, but for
+// subnormal scales, whose own rounding is coarser.
+//
+// Bound by instructions as much as by DRAM: 14 a value are what the measured
+// bandwidth leaves.  The loop over the rows is not unrolled, for the
+// instruction cache's sake; the next row is loaded ahead.
 template <int NG, bool BF16, bool VALUES>
 __global__ void __launch_bounds__(kRowThreads) write_kernel(Cache c, RowIo io) {
-    constexpr int D = NG * kGroup, N = kRows<NG>;
+    constexpr int D = NG * kGroup;
     if (blockIdx.x == 0) check_sequences(c);
     RowShare own;
     if (!row_share<NG>(c, &own)) return;
     const int sub = threadIdx.x & 7;                       // r
-    uint2 x[N][NG];
+    const bool here = own.t < c.total;
+    const uint16_t *k, *v;
     {
-        const bool here = own.t < c.total;
         const long long batch = c.cu != nullptr || !here ? 0 : own.t / c.S, row = here ? own.t - batch * c.S : 0;
-        const uint16_t* k = static_cast<const uint16_t*>(io.k) + batch * io.k_batch + row * io.k_row + sub * 4;
-        const uint16_t* v = static_cast<const uint16_t*>(io.v) + batch * io.v_batch + row * io.v_row + sub * 4;
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int y = own.first + i;
-            const uint16_t* src = y < c.Hkv ? k + y * io.k_head : v + (y - c.Hkv) * io.v_head;
-#pragma unroll
-            for (int g = 0; g < NG; ++g)
-                x[i][g] = i < own.n && here ? *reinterpret_cast<const uint2*>(src + g * kGroup) : make_uint2(0, 0);
-        }
+        k = static_cast<const uint16_t*>(io.k) + batch * io.k_batch + row * io.k_row + sub * 4;
+        v = static_cast<const uint16_t*>(io.v) + batch * io.v_batch + row * io.v_row + sub * 4;
     }
+    uint2 next[NG];
+    auto load = [&](int i) {
+        const int y = own.first + i;
+        const uint16_t* src = y < c.Hkv ? k + y * io.k_head : v + (y - c.Hkv) * io.v_head;
+#pragma unroll
+        for (int g = 0; g < NG; ++g)
+            next[g] = i < own.n && here ? *reinterpret_cast<const uint2*>(src + g * kGroup) : make_uint2(0, 0);
+    };
+    load(0);
     long long page = 0;
     int at = 0;
-    const RowPlace place = own.t < c.total ? place_of(c, own.t, &page, &at) : kRowSkip;
+    const RowPlace place = here ? place_of(c, own.t, &page, &at) : kRowSkip;
+#pragma unroll 1
+    for (int i = 0; i < own.n; ++i) {
+        const int y = own.first + i;
+        uint2 x[NG];
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        if (i >= own.n) break;
-        const int y = own.first + i, which = y >= c.Hkv ? 1 : 0, head = y - which * c.Hkv;
+        for (int g = 0; g < NG; ++g) x[g] = next[g];
+        load(i + 1);
         Words<NG> codes, scales;
         codes.clear();
         scales.clear();
         uint2 out[NG];
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
-            const uint32_t sb = group_scale<BF16>(x[i][g], sub);
+            const uint32_t sb = group_scale<BF16>(x[g], sub);
             const float s = bf16_bits(sb);
-            const bool some = sb != 0 && sb != 0x7fc0u;
-            // scales below 2^-64 are lifted by 2^96 (exactly) so that 1 / s is finite
-            const float lift = fabsf(s) < 5.42101086e-20f ? 7.92281625e28f : 1.f;
-            const float inv = some ? __frcp_rn(s * lift) : 0.f;
-            const float2 a = to_f32x2<BF16>(x[i][g].x), b = to_f32x2<BF16>(x[i][g].y);
-            const float e[4] = {a.x, a.y, b.x, b.y};
-            uint32_t word = 0;
+            const bool tiny = (sb & 0x7fffu) < 0x80u;      // zero or subnormal
+            float inv;
+            asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
+            if (tiny) inv = 0.f;
+            const float2 a = to_f32x2<BF16>(x[g].x), b = to_f32x2<BF16>(x[g].y);
+            float u[4] = {a.x * inv, a.y * inv, b.x * inv, b.y * inv};
+            if (__any_sync(0xffffffffu, tiny && sb != 0)) {
+                const float e[4] = {a.x, a.y, b.x, b.y};
+                const float lifted = __frcp_rn(s * 7.92281625e28f);   // 2^96
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (tiny && sb != 0) u[j] = fmaxf((e[j] * 7.92281625e28f) * lifted, -8.f);
+            }
+            int m[4];
             float q[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                float u = some ? (e[j] * lift) * inv : 0.f;
-                u = __fadd_rn(__fadd_rn(u, 768.f), -768.f);            // to multiples of 2^-14
-                u = fminf(fmaxf(u, -8.f), 7.f);
-                const float m = __fadd_rn(u, 12582920.f);              // 8 more than the nearest integer, ties to even
-                word |= (__float_as_uint(m) & 15u) << (4 * j);
-                if constexpr (VALUES) q[j] = __fadd_rn(m, -12582920.f) * s;
+                const float w = fminf(__fadd_rn(__fadd_rn(u[j], 768.f), -768.f), 7.f);   // to multiples of 2^-14
+                const float r = __fadd_rn(w, 12582920.f);       // 8 more than the nearest integer, ties to even
+                m[j] = __float_as_int(r);
+                if constexpr (VALUES) q[j] = __fadd_rn(r, -12582920.f) * s;
             }
+            // the integers sit in the low bits; what is above them leaves the low 16 bits of the sum
+            uint32_t word = static_cast<uint32_t>(m[0] + m[1] * 16 + m[2] * 256 + m[3] * 4096) & 0xffffu;
+            if (sb == 0x7fc0u) word = 0x8888u;
             codes.set(g, word);
             scales.set(g, sb);
             if constexpr (VALUES) out[g] = make_uint2(pack16<BF16>(q[0], q[1]), pack16<BF16>(q[2], q[3]));
         }
         if (place == kRowOk) {
-            const long long row = ((page * 2 + which) * c.Hkv + head) * c.P + at;
+            const long long row = (page * 2 * c.Hkv + y) * c.P + at;   // K's heads, then V's
             codes.store(c.codes + row * (16 * NG) + sub * (2 * NG));
             if (sub == 0) scales.store(c.scales + row * NG);
         }
         if constexpr (VALUES) {
             if (place != kRowSkip) {
-                uint16_t* dst = static_cast<uint16_t*>(which == 0 ? io.k_out : io.v_out) +
-                                (static_cast<long long>(own.t) * c.Hkv + head) * D;
+                uint16_t* to = static_cast<uint16_t*>(y < c.Hkv ? io.k_out : io.v_out) +
+                               (static_cast<long long>(own.t) * c.Hkv + (y < c.Hkv ? y : y - c.Hkv)) * D + sub * 4;
 #pragma unroll
                 for (int g = 0; g < NG; ++g)
-                    *reinterpret_cast<uint2*>(dst + g * kGroup + sub * 4) = place == kRowOk ? out[g] : make_uint2(0, 0);
+                    *reinterpret_cast<uint2*>(to + g * kGroup) = place == kRowOk ? out[g] : make_uint2(0, 0);
             }
         }
     }
