@@ -72,9 +72,10 @@ bool bad_strides(const long long* s, int unit) {
 }
 
 // Blocks of a launch over the call's rows, K and V of every head; 0: too many.
-template <int NG>
+template <int NG, int LANES>
 unsigned row_blocks(const kv4::Cache& c) {
-    const long long warps = (static_cast<long long>(c.total) + 3) / 4 * ((2LL * c.Hkv + kv4::kRows<NG> - 1) / kv4::kRows<NG>);
+    constexpr int TOK = 32 / LANES;
+    const long long warps = (static_cast<long long>(c.total) + TOK - 1) / TOK * ((2LL * c.Hkv + kv4::kRows<NG> - 1) / kv4::kRows<NG>);
     const long long blocks = (warps + kv4::kRowThreads / 32 - 1) / (kv4::kRowThreads / 32);
     return blocks > 0x7fffffffLL ? 0u : static_cast<unsigned>(blocks);
 }
@@ -282,7 +283,7 @@ int decode_any(int D, bool bf16, const kv4::Cache& c, const kv4::Attend& a, void
 
 template <int NG>
 int write(const kv4::Cache& c, const kv4::RowIo& io, bool bf16, cudaStream_t st) {
-    const unsigned blocks = row_blocks<NG>(c);
+    const unsigned blocks = row_blocks<NG, kv4::kWriteLanes>(c);
     if (blocks == 0) return FA_ERR_UNSUPPORTED;
     const bool values = io.k_out != nullptr;
     if (bf16) {
@@ -297,7 +298,7 @@ int write(const kv4::Cache& c, const kv4::RowIo& io, bool bf16, cudaStream_t st)
 
 template <int NG>
 int read(const kv4::Cache& c, const kv4::RowIo& io, bool bf16, cudaStream_t st) {
-    const unsigned blocks = row_blocks<NG>(c);
+    const unsigned blocks = row_blocks<NG, kv4::kReadLanes>(c);
     if (blocks == 0) return FA_ERR_UNSUPPORTED;
     if (bf16) kv4::read_kernel<NG, true><<<blocks, kv4::kRowThreads, 0, st>>>(c, io);
     else kv4::read_kernel<NG, false><<<blocks, kv4::kRowThreads, 0, st>>>(c, io);
@@ -327,7 +328,9 @@ int fa_kv4_write(const fa_kv4_cache_t* cache, const void* K, const void* V, cons
         bad_strides(k_strides, 4) || bad_strides(v_strides, 4))
         return FA_ERR_UNSUPPORTED;
     const kv4::RowIo io = {K, V, k_strides[0], k_strides[1], k_strides[2], v_strides[0], v_strides[1],
-                           v_strides[2], K_out, V_out};
+                           v_strides[2], K_out, V_out,
+                           !misaligned(K, 16) && !misaligned(V, 16) && !misaligned(K_out, 16) && !misaligned(V_out, 16) &&
+                               !bad_strides(k_strides, 8) && !bad_strides(v_strides, 8)};
 #define KV4_ONE(NG_) case NG_: return write<NG_>(c, io, dtype == FA_BF16, reinterpret_cast<cudaStream_t>(stream))
     switch (cache->D / kv4::kGroup) {
         KV4_ONE(1); KV4_ONE(2); KV4_ONE(3); KV4_ONE(4); KV4_ONE(5); KV4_ONE(6); KV4_ONE(7); KV4_ONE(8);

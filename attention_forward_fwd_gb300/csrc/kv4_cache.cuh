@@ -228,32 +228,37 @@ struct RowIo {
     long long k_batch, k_row, k_head, v_batch, v_row, v_head;
     void* k_out;     // contiguous [rows, Hkv, D]; may be null in a write
     void* v_out;
+    int wide;        // a write's addresses allow 16-byte accesses (else 8)
 };
 
-// Both kernels: a warp takes four tokens, 8 neighbouring threads each, and
-// kRows<NG> of their rows (K or V of a head) one after the other: where a token
-// lies is found once for all of them, while the first rows' loads are under
-// way.  Thread r of a row holds elements 4 r .. 4 r + 3 of every group: 8-byte
-// accesses to the 16-bit tensor, 64 contiguous bytes a group, and 2 NG
-// contiguous bytes of codes.  The four rows of an access are four tokens of the
-// same head, so that their scales fill whole sectors.
+// Both kernels: a warp takes 32 / LANES tokens, LANES neighbouring threads
+// each, and kRows<NG> of their rows (K or V of a head) one after the other: where
+// a token lies is found once for all of them, while the first row's loads are
+// under way.  The rows of an access are tokens of the same head, so that their
+// scales fill whole sectors.
+//  * read: 8 threads a row, thread r has elements 4 r .. 4 r + 3 of every group.
+//  * write: 4 threads a row, thread c has elements 8 c .. 8 c + 7, because the search
+//    for a group's extreme is paid once a thread and group, whatever they hold.
 constexpr int kRowThreads = 256;
 template <int NG>
 constexpr int kRows = NG <= 2 ? 8 : NG <= 4 ? 4 : 2;
+constexpr int kWriteLanes = 4, kReadLanes = 8;
 
 // Which rows a warp takes.
 struct RowShare {
     int t, first, n;      // token, first row (K's heads, then V's), rows
 };
-template <int NG>
+template <int NG, int LANES>
 __device__ __forceinline__ bool row_share(const Cache& c, RowShare* s) {
+    constexpr int TOK = 32 / LANES;
     const int rows = 2 * c.Hkv, chunks = (rows + kRows<NG> - 1) / kRows<NG>;
     const long long w = static_cast<long long>(blockIdx.x) * (kRowThreads / 32) + (threadIdx.x >> 5);
-    const long long t4 = w / chunks;
-    if (t4 >= (static_cast<long long>(c.total) + 3) / 4) return false;
-    s->first = static_cast<int>(w - t4 * chunks) * kRows<NG>;
+    const long long group = w / chunks;
+    if (group >= (static_cast<long long>(c.total) + TOK - 1) / TOK) return false;
+    s->first = static_cast<int>(w - group * chunks) * kRows<NG>;
     s->n = min(kRows<NG>, rows - s->first);
-    s->t = static_cast<int>(t4) * 4 + ((threadIdx.x >> 3) & 3);
+    const long long t = group * TOK + (threadIdx.x & 31) / LANES;
+    s->t = static_cast<int>(t < c.total ? t : c.total);   // total: none
     return true;
 }
 
@@ -273,29 +278,29 @@ __device__ __forceinline__ uint32_t min16x2(uint32_t a, uint32_t b) {
     return r;
 }
 
-// A group's scale (its bits) from its elements x (this thread's four), the
-// same in the group's 8 threads.
+// A group's scale (its bits) from its elements x (this thread's eight, two a
+// word), the same in the group's 4 threads.
 template <bool BF16>
-__device__ __forceinline__ uint32_t group_scale(uint2 x, int sub) {
+__device__ __forceinline__ uint32_t group_scale(const uint32_t* x, int sub) {
     // the largest x in the low half, the largest -x in the high half
-    const uint32_t up = max16x2<BF16>(x.x, x.y), down = min16x2<BF16>(x.x, x.y) ^ 0x80008000u;
+    const uint32_t up = max16x2<BF16>(max16x2<BF16>(x[0], x[1]), max16x2<BF16>(x[2], x[3]));
+    const uint32_t down = min16x2<BF16>(min16x2<BF16>(x[0], x[1]), min16x2<BF16>(x[2], x[3])) ^ 0x80008000u;
     uint32_t m = max16x2<BF16>(__byte_perm(up, down, 0x5410), __byte_perm(up, down, 0x7632));
 #pragma unroll
-    for (int i = 1; i < 8; i <<= 1) m = max16x2<BF16>(m, __shfl_xor_sync(0xffffffffu, m, i));
+    for (int i = 1; i < kWriteLanes; i <<= 1) m = max16x2<BF16>(m, __shfl_xor_sync(0xffffffffu, m, i));
     const float2 top = to_f32x2<BF16>(m);
     float xe = top.x > top.y ? top.x : -top.y;   // NaN if there is one
     const bool tie = top.x == top.y && top.x != 0.f;
     if (__any_sync(0xffffffffu, tie)) {
         // both signs at the largest magnitude: the first of them counts
-        const uint32_t e[4] = {x.x & 0xffffu, x.x >> 16, x.y & 0xffffu, x.y >> 16};
         uint32_t key = 0;
-#pragma unroll 1
-        for (int j = 0; j < 4; ++j) {
-            const uint32_t v = j == 0 ? e[0] : j == 1 ? e[1] : j == 2 ? e[2] : e[3];
-            key = max(key, ((v & 0x7fffu) << 16) | ((31u - (sub * 4 + j)) << 1) | (v >> 15));
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const uint32_t v = (j & 1) ? x[j / 2] >> 16 : x[j / 2] & 0xffffu;
+            key = max(key, ((v & 0x7fffu) << 16) | ((31u - (sub * 8 + j)) << 1) | (v >> 15));
         }
-#pragma unroll 1
-        for (int i = 1; i < 8; i <<= 1) key = max(key, __shfl_xor_sync(0xffffffffu, key, i));
+#pragma unroll
+        for (int i = 1; i < kWriteLanes; i <<= 1) key = max(key, __shfl_xor_sync(0xffffffffu, key, i));
         if (tie && (key & 1u) == 0) xe = top.x;
     }
     const uint32_t sb = pack16<true>(xe * -0.125f, 0.f) & 0xffffu;
@@ -318,22 +323,35 @@ __global__ void __launch_bounds__(kRowThreads) write_kernel(Cache c, RowIo io) {
     constexpr int D = NG * kGroup;
     if (blockIdx.x == 0) check_sequences(c);
     RowShare own;
-    if (!row_share<NG>(c, &own)) return;
-    const int sub = threadIdx.x & 7;                       // r
+    if (!row_share<NG, kWriteLanes>(c, &own)) return;
+    const int sub = threadIdx.x & (kWriteLanes - 1);       // c
     const bool here = own.t < c.total;
     const uint16_t *k, *v;
     {
         const long long batch = c.cu != nullptr || !here ? 0 : own.t / c.S, row = here ? own.t - batch * c.S : 0;
-        k = static_cast<const uint16_t*>(io.k) + batch * io.k_batch + row * io.k_row + sub * 4;
-        v = static_cast<const uint16_t*>(io.v) + batch * io.v_batch + row * io.v_row + sub * 4;
+        k = static_cast<const uint16_t*>(io.k) + batch * io.k_batch + row * io.k_row + sub * 8;
+        v = static_cast<const uint16_t*>(io.v) + batch * io.v_batch + row * io.v_row + sub * 8;
     }
-    uint2 next[NG];
+    uint4 next[NG];
     auto load = [&](int i) {
         const int y = own.first + i;
         const uint16_t* src = y < c.Hkv ? k + y * io.k_head : v + (y - c.Hkv) * io.v_head;
+        const bool on = i < own.n && here;
+        if (io.wide) {
 #pragma unroll
-        for (int g = 0; g < NG; ++g)
-            next[g] = i < own.n && here ? *reinterpret_cast<const uint2*>(src + g * kGroup) : make_uint2(0, 0);
+            for (int g = 0; g < NG; ++g)
+                next[g] = on ? *reinterpret_cast<const uint4*>(src + g * kGroup) : make_uint4(0, 0, 0, 0);
+        } else {
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                next[g] = make_uint4(0, 0, 0, 0);
+                if (on) {
+                    const uint2 lo = *reinterpret_cast<const uint2*>(src + g * kGroup);
+                    const uint2 hi = *reinterpret_cast<const uint2*>(src + g * kGroup + 4);
+                    next[g] = make_uint4(lo.x, lo.y, hi.x, hi.y);
+                }
+            }
+        }
     };
     load(0);
     long long page = 0;
@@ -342,59 +360,77 @@ __global__ void __launch_bounds__(kRowThreads) write_kernel(Cache c, RowIo io) {
 #pragma unroll 1
     for (int i = 0; i < own.n; ++i) {
         const int y = own.first + i;
-        uint2 x[NG];
+        uint4 x[NG];
 #pragma unroll
         for (int g = 0; g < NG; ++g) x[g] = next[g];
         load(i + 1);
-        Words<NG> codes, scales;
+        Words<2 * NG> codes;
+        Words<NG> scales;
         codes.clear();
         scales.clear();
-        uint2 out[NG];
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
-            const uint32_t sb = group_scale<BF16>(x[g], sub);
+            const uint32_t e[4] = {x[g].x, x[g].y, x[g].z, x[g].w};
+            const uint32_t sb = group_scale<BF16>(e, sub);
             const float s = bf16_bits(sb);
             const bool tiny = (sb & 0x7fffu) < 0x80u;      // zero or subnormal
             float inv;
             asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
             if (tiny) inv = 0.f;
-            const float2 a = to_f32x2<BF16>(x[g].x), b = to_f32x2<BF16>(x[g].y);
-            float u[4] = {a.x * inv, a.y * inv, b.x * inv, b.y * inv};
-            if (__any_sync(0xffffffffu, tiny && sb != 0)) {
-                const float e[4] = {a.x, a.y, b.x, b.y};
-                const float lifted = __frcp_rn(s * 7.92281625e28f);   // 2^96
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (tiny && sb != 0) u[j] = fmaxf((e[j] * 7.92281625e28f) * lifted, -8.f);
-            }
-            int m[4];
-            float q[4];
+            float u[8];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
+                const float2 f = to_f32x2<BF16>(e[j]);
+                u[2 * j] = f.x * inv;
+                u[2 * j + 1] = f.y * inv;
+            }
+            if (__any_sync(0xffffffffu, tiny && sb != 0)) {
+                const float lifted = __frcp_rn(s * 7.92281625e28f);   // 2^96
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float2 f = to_f32x2<BF16>(e[j / 2]);
+                    if (tiny && sb != 0) u[j] = fmaxf(((j & 1) ? f.y : f.x) * 7.92281625e28f * lifted, -8.f);
+                }
+            }
+            int m[8];
+            float q[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
                 const float w = fminf(__fadd_rn(__fadd_rn(u[j], 768.f), -768.f), 7.f);   // to multiples of 2^-14
                 const float r = __fadd_rn(w, 12582920.f);       // 8 more than the nearest integer, ties to even
                 m[j] = __float_as_int(r);
                 if constexpr (VALUES) q[j] = __fadd_rn(r, -12582920.f) * s;
             }
-            // the integers sit in the low bits; what is above them leaves the low 16 bits of the sum
-            uint32_t word = static_cast<uint32_t>(m[0] + m[1] * 16 + m[2] * 256 + m[3] * 4096) & 0xffffu;
-            if (sb == 0x7fc0u) word = 0x8888u;
-            codes.set(g, word);
+            // the integers sit in the low bits; what is above them leaves the low 16 bits of the sums
+            uint32_t w0 = static_cast<uint32_t>(m[0] + m[1] * 16 + m[2] * 256 + m[3] * 4096) & 0xffffu;
+            uint32_t w1 = static_cast<uint32_t>(m[4] + m[5] * 16 + m[6] * 256 + m[7] * 4096) & 0xffffu;
+            if (sb == 0x7fc0u) w0 = w1 = 0x8888u;
+            codes.set(g, w0);          // r = 2 c
+            codes.set(NG + g, w1);     // r = 2 c + 1
             scales.set(g, sb);
-            if constexpr (VALUES) out[g] = make_uint2(pack16<BF16>(q[0], q[1]), pack16<BF16>(q[2], q[3]));
+            if constexpr (VALUES)
+                x[g] = make_uint4(pack16<BF16>(q[0], q[1]), pack16<BF16>(q[2], q[3]), pack16<BF16>(q[4], q[5]),
+                                  pack16<BF16>(q[6], q[7]));
         }
         if (place == kRowOk) {
             const long long row = (page * 2 * c.Hkv + y) * c.P + at;   // K's heads, then V's
-            codes.store(c.codes + row * (16 * NG) + sub * (2 * NG));
+            codes.store(c.codes + row * (16 * NG) + sub * (4 * NG));
             if (sub == 0) scales.store(c.scales + row * NG);
         }
         if constexpr (VALUES) {
             if (place != kRowSkip) {
                 uint16_t* to = static_cast<uint16_t*>(y < c.Hkv ? io.k_out : io.v_out) +
-                               (static_cast<long long>(own.t) * c.Hkv + (y < c.Hkv ? y : y - c.Hkv)) * D + sub * 4;
+                               (static_cast<long long>(own.t) * c.Hkv + (y < c.Hkv ? y : y - c.Hkv)) * D + sub * 8;
 #pragma unroll
-                for (int g = 0; g < NG; ++g)
-                    *reinterpret_cast<uint2*>(to + g * kGroup) = place == kRowOk ? out[g] : make_uint2(0, 0);
+                for (int g = 0; g < NG; ++g) {
+                    const uint4 o = place == kRowOk ? x[g] : make_uint4(0, 0, 0, 0);
+                    if (io.wide) {
+                        *reinterpret_cast<uint4*>(to + g * kGroup) = o;
+                    } else {
+                        *reinterpret_cast<uint2*>(to + g * kGroup) = make_uint2(o.x, o.y);
+                        *reinterpret_cast<uint2*>(to + g * kGroup + 4) = make_uint2(o.z, o.w);
+                    }
+                }
             }
         }
     }
@@ -426,7 +462,7 @@ __global__ void __launch_bounds__(kRowThreads) read_kernel(Cache c, RowIo io) {
     constexpr int D = NG * kGroup, N = kRows<NG>;
     if (blockIdx.x == 0) check_sequences(c);
     RowShare own;
-    if (!row_share<NG>(c, &own) || own.t >= c.total) return;
+    if (!row_share<NG, kReadLanes>(c, &own) || own.t >= c.total) return;
     const int sub = threadIdx.x & 7;
     long long page = 0;
     int at = 0;

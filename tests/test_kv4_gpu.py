@@ -177,6 +177,15 @@ def test_write_takes_slices_of_a_projection(fa):
     fa.kv4_write(qkv[:, :, 4:6], qkv[:, :, 6:8], **c)
     np.testing.assert_array_equal(c["codes"].cpu().numpy(), s.codes)
     np.testing.assert_array_equal(host(c["scales"]), s.scales)
+    # addresses that allow 8-byte accesses only
+    flat = torch.zeros(qkv.numel() + 4, dtype=qkv.dtype, device="cuda")
+    flat[4:] = qkv.flatten()
+    odd = flat[4:].view(qkv.shape)
+    w = {**c, "codes": torch.zeros_like(c["codes"]), "scales": torch.zeros_like(c["scales"])}
+    fa.kv4_write(odd[:, :, 4:6], odd[:, :, 6:8], **w)
+    z = {**c, "codes": torch.zeros_like(c["codes"]), "scales": torch.zeros_like(c["scales"])}
+    fa.kv4_write(qkv[:, :, 4:6], qkv[:, :, 6:8], **z)
+    assert torch.equal(w["codes"], z["codes"]) and torch.equal(w["scales"], z["scales"])
     # heads in front of rows: [B, H, S, D] seen as [B, S, H, D]
     t = qkv[:, :, 4:6].transpose(1, 2).contiguous().transpose(1, 2)
     fa.kv4_write(t, qkv[:, :, 6:8], **c)
