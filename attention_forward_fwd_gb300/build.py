@@ -43,6 +43,66 @@ def _sources():
 
 STAMP_PATH = LIB_PATH + ".sha256"
 
+# The native marshalling of the cache calls (csrc/fa_binding.cpp): a Python
+# extension against the installed torch.  Without it (no compiler or headers
+# for it) the same calls are marshalled in Python.
+BINDING_PATH = os.path.join(PKG_DIR, "fa_binding.so")
+BINDING_SOURCE = os.path.join(CSRC, "fa_binding.cpp")
+
+
+def binding_command() -> list[str]:
+    import sysconfig
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include")
+    lib = os.path.join(root, "lib")
+    include = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+               sysconfig.get_paths()["include"], cuda, INCLUDE]
+    return [os.environ.get("CXX") or shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            *[x for d in include for x in ("-isystem", d)], BINDING_SOURCE, "-o", BINDING_PATH + ".tmp",
+            "-L" + lib, "-Wl,-rpath," + lib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+
+
+def binding_stamp() -> str:
+    """What a built binding belongs to: its sources, this Python, torch and machine."""
+    import hashlib
+    import platform
+    import sys
+    import torch
+    h = hashlib.sha256(f"{sys.version}|{torch.__version__}|{platform.machine()}".encode())
+    for path in (BINDING_SOURCE, os.path.join(INCLUDE, "fa_gb300.h")):
+        with open(path, "rb") as f:
+            h.update(f.read())
+    return h.hexdigest()
+
+
+def binding_built() -> bool:
+    stamp = BINDING_PATH + ".sha256"
+    if not (os.path.exists(BINDING_PATH) and os.path.exists(stamp)):
+        return False
+    with open(stamp) as f:
+        return f.read().strip() == binding_stamp()
+
+
+def _start_binding():
+    """The running compiler, or None (the binding is built, or cannot be)."""
+    try:
+        if binding_built():
+            return None
+        os.makedirs(os.path.join(ROOT, "_build"), exist_ok=True)
+        log = open(os.path.join(ROOT, "_build", "binding.txt"), "w")
+        return subprocess.Popen(binding_command(), stdout=log, stderr=subprocess.STDOUT)
+    except (ImportError, OSError, RuntimeError):
+        return None
+
+
+def _finish_binding(run) -> None:
+    if run is not None and run.wait() == 0:
+        os.replace(BINDING_PATH + ".tmp", BINDING_PATH)
+        with open(BINDING_PATH + ".sha256", "w") as f:
+            f.write(binding_stamp() + "\n")
+
 
 def source_hash(debug: bool = False) -> str:
     """SHA-256 over the library's sources (names and contents), the compile
@@ -122,6 +182,14 @@ def build(force: bool = False, verbose: bool = False, debug: bool = False) -> st
     """Compile the library unless it exists with the stamp of the current
     sources; ``debug`` builds libfa_gb300_debug.so, the same sources with the
     device-side invariant checks (FA_DEBUG = 1)."""
+    binding = None if debug else _start_binding()
+    try:
+        return _build_library(force, verbose, debug)
+    finally:
+        _finish_binding(binding)
+
+
+def _build_library(force: bool, verbose: bool, debug: bool) -> str:
     lib = DEBUG_LIB_PATH if debug else LIB_PATH
     if not force and not needs_build(debug):
         return lib

@@ -23,8 +23,9 @@ import attention_forward_fwd_gb300 as _fa
 KV4_GROUP = 32   # values that share a scale
 
 # A decoding step makes these calls for every layer and its kernels take
-# microseconds, so the calls look at each property of a tensor once, in one
-# expression, and find out what was wrong only when that fails.
+# microseconds.  So the common case goes through csrc/fa_binding.cpp, and the code
+# here (other devices and streams, and what does not fit) looks at each property of a tensor
+# once, in one expression, and finds out what was wrong only when that fails.
 _pack_cache = struct.Struct("@5P8i").pack      # fa_kv4_cache_t
 _pack3 = struct.Struct("@3q").pack             # strides
 _pack2 = struct.Struct("@2q").pack
@@ -35,12 +36,33 @@ _torch = None
 
 
 def _lib():
-    """The library; torch too, which the package does not import by itself."""
-    global _torch
+    """The library; torch too, which the package does not import by itself, and the
+    native marshalling where it has been built."""
+    global _torch, _native
     if _torch is None:
         import torch
         _torch = torch
+        lib = _fa.library()
+        _native = _load_native(lib)
     return _fa._LIB or _fa.library()
+
+
+_native = None   # csrc/fa_binding.cpp
+
+
+def _load_native(lib):
+    import importlib.machinery
+    import importlib.util
+
+    from .build import BINDING_PATH, binding_built
+    if not binding_built():
+        return None
+    loader = importlib.machinery.ExtensionFileLoader("fa_binding", BINDING_PATH)
+    module = importlib.util.module_from_spec(importlib.util.spec_from_loader("fa_binding", loader))
+    loader.exec_module(module)
+    module.init(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+        lib.fa_kv4_write, lib.fa_kv4_read, lib.fa_kv4_attention_workspace_size, lib.fa_kv4_attention, lib.fa_rotary)))
+    return module
 
 
 def _need(ok, what):
@@ -197,6 +219,10 @@ def kv4_write(k, v, codes, scales, page_table, seq_lens, cu_seqlens=None, max_se
     the current one) and not waited for.
     """
     lib = _lib()
+    if stream is None and _native is not None:
+        rc = _native.kv4_write(k, v, codes, scales, page_table, seq_lens, cu_seqlens, max_seqlen, k_out, v_out)
+        if rc is not NotImplemented:
+            return _check(rc, "fa_kv4_write") if rc is not None else None
     dev, packed, shape = codes.device, cu_seqlens is not None, k.shape
     dtype = _code(k.dtype)
     _need(v.dtype is k.dtype and v.shape == shape and len(shape) >= 3, "k and v must be alike")
@@ -231,6 +257,14 @@ def kv4_read(codes, scales, page_table, seq_lens, cu_seqlens=None, max_seqlen=No
     given, else not defined).
     """
     lib = _lib()
+    if stream is None and k_out is None and v_out is None and _native is not None and \
+            (dtype is None or dtype is _torch.bfloat16 or dtype is _torch.float16):
+        r = _native.kv4_read(codes, scales, page_table, seq_lens, cu_seqlens, max_seqlen,
+                             max_seqlen if cu_seqlens is None else total, dtype is not _torch.float16)
+        if type(r) is tuple:
+            return r
+        if r is not NotImplemented:
+            _check(r, "fa_kv4_read")
     dev = codes.device
     if cu_seqlens is None:
         _need(max_seqlen is not None, "max_seqlen (the rows of a sequence) is needed without cu_seqlens")
@@ -291,6 +325,13 @@ def kv4_attention(q, codes, scales, page_table, seq_lens, cu_seqlens=None, max_s
     [H, total].  The workspace is made anew for each call.
     """
     lib = _lib()
+    if stream is None and _native is not None:
+        r = _native.kv4_attention(q, codes, scales, page_table, seq_lens, cu_seqlens, max_seqlen, window_left, scale,
+                                  out, lse, bool(with_lse))
+        if type(r) is tuple:
+            return r
+        if r is not NotImplemented:
+            _check(r, "fa_kv4_attention")
     dev, packed, shape = codes.device, cu_seqlens is not None, q.shape
     dtype = _code(q.dtype)
     _need(len(shape) >= 3, "q must be [B, S, H, D], or [total, H, D] with cu_seqlens")
@@ -395,6 +436,12 @@ def rotary(q, positions, inv_freq, axes, k=None, interleaved: bool = False, inve
     given (``q_out=q``: in place).
     """
     lib = _lib()
+    if stream is None and _native is not None:
+        r = _native.rotary(q, positions, inv_freq, axes, k, interleaved, inverse, q_out, k_out)
+        if type(r) is int:
+            _check(r, "fa_rotary")
+        elif r is not NotImplemented:
+            return r
     torch = _torch
     dev, shape, F, psh = positions.device, q.shape, inv_freq.numel(), positions.shape
     dtype = _code(q.dtype)
