@@ -71,11 +71,17 @@ bool bad_strides(const long long* s, int unit) {
     return s[0] % unit != 0 || s[1] % unit != 0 || s[2] % unit != 0;
 }
 
-// Blocks of a launch over the call's rows, K and V of every head; 0: too many.
+// Blocks of a launch over the call's rows, K and V of every head (0: too
+// many), and how many of a token's rows a warp takes: one while that does not fill
+// the GPU (16 warps an SM; a step of 64 tokens, 16 rows each: 8.2 us with four
+// rows a warp, one after the other, 3.1 us with one), up to kRows where the
+// search for the token's place is to be shared.
 template <int NG, int LANES>
-unsigned row_blocks(const kv4::Cache& c) {
+unsigned row_blocks(const kv4::Cache& c, int* per) {
     constexpr int TOK = 32 / LANES;
-    const long long warps = (static_cast<long long>(c.total) + TOK - 1) / TOK * ((2LL * c.Hkv + kv4::kRows<NG> - 1) / kv4::kRows<NG>);
+    const long long groups = (static_cast<long long>(c.total) + TOK - 1) / TOK, rows = 2LL * c.Hkv;
+    *per = static_cast<int>(std::max<long long>(1, std::min<long long>(kv4::kRows<NG>, groups * rows / (152 * 16))));
+    const long long warps = groups * ((rows + *per - 1) / *per);
     const long long blocks = (warps + kv4::kRowThreads / 32 - 1) / (kv4::kRowThreads / 32);
     return blocks > 0x7fffffffLL ? 0u : static_cast<unsigned>(blocks);
 }
@@ -282,8 +288,8 @@ int decode_any(int D, bool bf16, const kv4::Cache& c, const kv4::Attend& a, void
 }
 
 template <int NG>
-int write(const kv4::Cache& c, const kv4::RowIo& io, bool bf16, cudaStream_t st) {
-    const unsigned blocks = row_blocks<NG, kv4::kWriteLanes>(c);
+int write(const kv4::Cache& c, kv4::RowIo io, bool bf16, cudaStream_t st) {
+    const unsigned blocks = row_blocks<NG, kv4::kWriteLanes>(c, &io.per);
     if (blocks == 0) return FA_ERR_UNSUPPORTED;
     const bool values = io.k_out != nullptr;
     if (bf16) {
@@ -297,8 +303,8 @@ int write(const kv4::Cache& c, const kv4::RowIo& io, bool bf16, cudaStream_t st)
 }
 
 template <int NG>
-int read(const kv4::Cache& c, const kv4::RowIo& io, bool bf16, cudaStream_t st) {
-    const unsigned blocks = row_blocks<NG, kv4::kReadLanes>(c);
+int read(const kv4::Cache& c, kv4::RowIo io, bool bf16, cudaStream_t st) {
+    const unsigned blocks = row_blocks<NG, kv4::kReadLanes>(c, &io.per);
     if (blocks == 0) return FA_ERR_UNSUPPORTED;
     if (bf16) kv4::read_kernel<NG, true><<<blocks, kv4::kRowThreads, 0, st>>>(c, io);
     else kv4::read_kernel<NG, false><<<blocks, kv4::kRowThreads, 0, st>>>(c, io);
@@ -330,7 +336,8 @@ int fa_kv4_write(const fa_kv4_cache_t* cache, const void* K, const void* V, cons
     const kv4::RowIo io = {K, V, k_strides[0], k_strides[1], k_strides[2], v_strides[0], v_strides[1],
                            v_strides[2], K_out, V_out,
                            !misaligned(K, 16) && !misaligned(V, 16) && !misaligned(K_out, 16) && !misaligned(V_out, 16) &&
-                               !bad_strides(k_strides, 8) && !bad_strides(v_strides, 8)};
+                               !bad_strides(k_strides, 8) && !bad_strides(v_strides, 8),
+                           1};
 #define KV4_ONE(NG_) case NG_: return write<NG_>(c, io, dtype == FA_BF16, reinterpret_cast<cudaStream_t>(stream))
     switch (cache->D / kv4::kGroup) {
         KV4_ONE(1); KV4_ONE(2); KV4_ONE(3); KV4_ONE(4); KV4_ONE(5); KV4_ONE(6); KV4_ONE(7); KV4_ONE(8);

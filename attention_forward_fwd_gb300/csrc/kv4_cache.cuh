@@ -229,10 +229,11 @@ struct RowIo {
     void* k_out;     // contiguous [rows, Hkv, D]; may be null in a write
     void* v_out;
     int wide;        // a write's addresses allow 16-byte accesses (else 8)
+    int per;         // rows a warp takes of each of its tokens, at most kRows
 };
 
 // Both kernels: a warp takes 32 / LANES tokens, LANES neighbouring threads
-// each, and kRows<NG> of their rows (K or V of a head) one after the other: where
+// each, and up to kRows<NG> of their rows (K or V of a head) one after the other: where
 // a token lies is found once for all of them, while the first row's loads are
 // under way.  The rows of an access are tokens of the same head, so that their
 // scales fill whole sectors.
@@ -248,15 +249,15 @@ constexpr int kWriteLanes = 4, kReadLanes = 8;
 struct RowShare {
     int t, first, n;      // token, first row (K's heads, then V's), rows
 };
-template <int NG, int LANES>
-__device__ __forceinline__ bool row_share(const Cache& c, RowShare* s) {
+template <int LANES>
+__device__ __forceinline__ bool row_share(const Cache& c, int per, RowShare* s) {
     constexpr int TOK = 32 / LANES;
-    const int rows = 2 * c.Hkv, chunks = (rows + kRows<NG> - 1) / kRows<NG>;
+    const int rows = 2 * c.Hkv, chunks = (rows + per - 1) / per;
     const long long w = static_cast<long long>(blockIdx.x) * (kRowThreads / 32) + (threadIdx.x >> 5);
     const long long group = w / chunks;
     if (group >= (static_cast<long long>(c.total) + TOK - 1) / TOK) return false;
-    s->first = static_cast<int>(w - group * chunks) * kRows<NG>;
-    s->n = min(kRows<NG>, rows - s->first);
+    s->first = static_cast<int>(w - group * chunks) * per;
+    s->n = min(per, rows - s->first);
     const long long t = group * TOK + (threadIdx.x & 31) / LANES;
     s->t = static_cast<int>(t < c.total ? t : c.total);   // total: none
     return true;
@@ -323,7 +324,7 @@ __global__ void __launch_bounds__(kRowThreads) write_kernel(Cache c, RowIo io) {
     constexpr int D = NG * kGroup;
     if (blockIdx.x == 0) check_sequences(c);
     RowShare own;
-    if (!row_share<NG, kWriteLanes>(c, &own)) return;
+    if (!row_share<kWriteLanes>(c, io.per, &own)) return;
     const int sub = threadIdx.x & (kWriteLanes - 1);       // c
     const bool here = own.t < c.total;
     const uint16_t *k, *v;
@@ -462,7 +463,7 @@ __global__ void __launch_bounds__(kRowThreads) read_kernel(Cache c, RowIo io) {
     constexpr int D = NG * kGroup, N = kRows<NG>;
     if (blockIdx.x == 0) check_sequences(c);
     RowShare own;
-    if (!row_share<NG, kReadLanes>(c, &own) || own.t >= c.total) return;
+    if (!row_share<kReadLanes>(c, io.per, &own) || own.t >= c.total) return;
     const int sub = threadIdx.x & 7;
     long long page = 0;
     int at = 0;
