@@ -44,8 +44,9 @@ int check_cache(const fa_kv4_cache_t* d, int dtype, kv4::Cache* c) {
     if (d->D < kv4::kGroup || d->D > 8 * kv4::kGroup || d->D % kv4::kGroup != 0) return FA_ERR_UNSUPPORTED;
     if (d->page_size % 16 != 0) return FA_ERR_UNSUPPORTED;
     // rows, tokens of the cache and tokens of a sequence are numbered with an int
+    // (and a few tiles past the last token are looked at)
     if (total > 0x7fffffffLL - 4 || static_cast<long long>(d->pages) * d->page_size > 0x7fffffffLL ||
-        static_cast<long long>(d->max_pages) * d->page_size > 0x7fffffffLL - 64)
+        static_cast<long long>(d->max_pages) * d->page_size > 0x7fffffffLL - 4096)
         return FA_ERR_UNSUPPORTED;
     if (misaligned(d->codes, 16) || misaligned(d->scales, 16) || misaligned(d->page_table, 4) ||
         misaligned(d->seq_lens, 4) || misaligned(d->cu_seqlens, 4))

@@ -285,7 +285,8 @@ def test_packed_sequences(fa, dtype, D, H_kv, G, P):
 
 
 @pytest.mark.parametrize("B,L,H_kv,G,D,P", [(1, 9000, 1, 4, 128, 64), (1, 4097, 2, 8, 64, 16), (3, 2500, 1, 2, 256, 32),
-                                            (40, 200, 2, 2, 64, 16), (150, 70, 1, 1, 32, 16)])
+                                            (40, 200, 2, 2, 64, 16), (150, 70, 1, 1, 32, 16),
+                                            (300, 620, 1, 2, 32, 16)])
 def test_ranges_that_cut_items(fa, B, L, H_kv, G, D, P):
     """Long contexts over many CTAs, many short ones in a CTA."""
     lens = [max(0, L - 37 * b % L) for b in range(B)]
@@ -561,3 +562,72 @@ def test_offsets_past_32_bits(fa):
     ro, rl, ra = kv4.attention(decode(q16[0], "bf16"), s.rows(0, 0), s.rows(0, 1), D ** -0.5)
     to, tl = attention_tolerance(decode(q16[0], "bf16"), s.rows(0, 0), ro, ra, rl, D ** -0.5, "bf16")
     assert (np.abs(decode(host(o[0]), "bf16") - ro) <= to).all()
+
+
+def test_both_ways_of_marshalling_agree(fa, monkeypatch):
+    """The native binding and the Python code make the same calls: results bit
+    for bit, refusals alike."""
+    import torch
+    from attention_forward_fwd_gb300 import cache
+    s = Setup([130, 7, 0], 2, 64, 16, seed=21)
+    c = s.cuda()
+    cu = torch.tensor([0, 100, 103, 103], dtype=torch.int32, device="cuda")
+    qkv = dev(to16(s.r.standard_normal((103, 10, 64)), "bf16"), "bf16")
+    freq, axes = fa.rotary_frequencies(64, (16, 16))
+    pos = torch.arange(206, dtype=torch.int32, device="cuda").view(103, 2)
+
+    def calls():
+        w = {**c, "codes": c["codes"].clone(), "scales": c["scales"].clone()}
+        kw = dict(cu_seqlens=cu, max_seqlen=100)
+        q, k = fa.rotary(qkv[:, :6], pos, freq, axes, k=qkv[:, 6:8])
+        (one,) = [fa.rotary(qkv[:, :6], pos, freq, axes, interleaved=True, inverse=True)]
+        v = qkv[:, 8:]
+        ko, vo = torch.empty_like(k), torch.empty(v.shape, dtype=v.dtype, device="cuda")
+        assert fa.kv4_write(k, v, **w, **kw, k_out=ko, v_out=vo) is None
+        out = [q, k, one, ko, vo, w["codes"], w["scales"], *fa.kv4_read(**w, **kw, total=103)]
+        out += [*fa.kv4_read(**w, max_seqlen=5, dtype=torch.float16)]
+        out += [*fa.kv4_attention(q, **w, **kw), *fa.kv4_attention(q, **w, **kw, window_left=9, scale=0.5)]
+        o = torch.empty(q.shape, dtype=q.dtype, device="cuda")
+        p, none = fa.kv4_attention(q, **w, **kw, out=o, with_lse=False)
+        assert p.data_ptr() == o.data_ptr() and none is None
+        b = qkv[:3, :6].unsqueeze(1)
+        out += [o, *fa.kv4_attention(b, **w), fa.rotary(b, pos[:3].unsqueeze(1), freq, axes)]
+        for bad in (lambda: fa.kv4_attention(q[:, :5], **w, **kw), lambda: fa.kv4_attention(q.float(), **w, **kw),
+                    lambda: fa.kv4_write(k, v[:50], **w, **kw), lambda: fa.kv4_attention(q, **w),
+                    lambda: fa.rotary(q, pos.long(), freq, axes), lambda: fa.rotary(q, pos, freq, axes.long()),
+                    lambda: fa.kv4_read(**{**w, "seq_lens": w["seq_lens"].long()}, max_seqlen=3),
+                    lambda: fa.kv4_read(**w, cu_seqlens=cu), lambda: fa.kv4_attention(q, **w, **kw, out=o[:50]),
+                    lambda: fa.kv4_attention(q.cpu(), **w, **kw)):
+            with pytest.raises(ValueError):
+                bad()
+        for bad in (lambda: fa.kv4_attention(q, **w, **kw, window_left=-2), lambda: fa.kv4_attention(q, **w, **kw, scale=-1.0)):
+            with pytest.raises(fa.FaError):
+                bad()
+        return out
+
+    first = calls()
+    monkeypatch.setattr(cache, "_native", None)
+    for x, y in zip(first, calls(), strict=True):
+        assert x.shape == y.shape and x.dtype == y.dtype and x.is_contiguous()
+        assert torch.equal(x.view(torch.uint8) if x.dtype == torch.uint8 else torch.nan_to_num(x.float()),
+                           y.view(torch.uint8) if y.dtype == torch.uint8 else torch.nan_to_num(y.float()))
+
+
+def test_two_streams_at_once(fa):
+    """Calls that overlap on two streams, cut and whole, steps and prompts,
+    give what they give alone."""
+    import torch
+    s = Setup([5000, 300, 900], 2, 64, 16, seed=22)
+    c = s.cuda()
+    qs = [dev(to16(s.r.standard_normal((3, n, 4, 64)), "f16"), "f16") for n in (1, 1, 60, 40)]
+    alone = [fa.kv4_attention(q, **c) for q in qs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in qs]
+    for _ in range(5):
+        got = []
+        for q, st in zip(qs, streams):
+            with torch.cuda.stream(st):
+                got.append(fa.kv4_attention(q, **c))
+        torch.cuda.synchronize()
+        for (a, al), (b, bl) in zip(alone, got):
+            assert torch.equal(a, b) and torch.equal(al, bl)
