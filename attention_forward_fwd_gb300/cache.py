@@ -3,9 +3,10 @@
 A decoding step turns its q and k (``rotary``), writes k and v into the cache
 (``kv4_write``) and attends over it (``kv4_attention``); ``kv4_read`` gives
 plain K and V back, for the other attention calls.  As in the rest of the
-package this module only marshals arguments; the work runs in the library's
-kernels (``fa_kv4_*`` and ``fa_rotary`` in ``include/fa_gb300.h``, where the
-cache's format and the checks on the device are described).
+package this module only marshals arguments (and records nothing for
+autograd); the work runs in the library's kernels (``fa_kv4_*`` and
+``fa_rotary`` in ``include/fa_gb300.h``, where the cache's format and the checks
+on the device are described).
 
 Every call takes ``page_table`` (int32 [B, max_pages]) and ``seq_lens`` (int32
 [B], the tokens in the cache with the call's own), and concerns the LAST rows of
@@ -346,6 +347,7 @@ def kv4_attention(q, codes, scales, page_table, seq_lens, cu_seqlens=None, max_s
     if lse is not None:
         _need(lse.shape == lse_shape and lse.dtype is _torch.float32 and lse.is_contiguous() and lse.device == dev,
               f"lse must be a contiguous fp32 tensor {lse_shape}")
+    window = max(-2, min(int(window_left), 0x7fffffff))   # a C int; positions are below that
     handle, on = _enter(dev, stream)
     try:
         if out is None:
@@ -358,7 +360,7 @@ def kv4_attention(q, codes, scales, page_table, seq_lens, cu_seqlens=None, max_s
             # not kept: two captured graphs never share one
             ws = _torch.empty(n, dtype=_torch.uint8, device=dev) if n else None
             rc = lib.fa_kv4_attention(c, q.data_ptr(), qs, out.data_ptr(), lse.data_ptr() if lse is not None else None,
-                                      H, int(window_left), D ** -0.5 if scale is None else float(scale), dtype,
+                                      H, window, D ** -0.5 if scale is None else float(scale), dtype,
                                       ws.data_ptr() if n else None, n, handle)
     finally:
         if on is not None:
@@ -480,6 +482,7 @@ def rotary(q, positions, inv_freq, axes, k=None, interleaved: bool = False, inve
         if not H:
             first, second = second, _NO_TENSOR
         rc, T = _fa.FA_OK, positions.numel() // A
+        _need(max(T, A, H, H2) <= 0x7fffffff, "sizes must fit 32 bits")
         if T and H + H2:
             rc = lib.fa_rotary(*first, *second, positions.data_ptr(), inv_freq.data_ptr(), axes.data_ptr(), T, A, F,
                                D, 1 if interleaved else 0, 1 if inverse else 0, dtype, handle)

@@ -237,7 +237,7 @@ bool tokens_of(const at::Tensor& t, long long* strides) {
 // q, positions, inv_freq, axes, k, interleaved, inverse, q_out, k_out -> q_out or (q_out, k_out)
 PyObject* rotary(PyObject*, PyObject* const* a, Py_ssize_t n) {
     try {
-        if (n != 9) return not_here();
+        if (n != 9 || !PyBool_Check(a[5]) || !PyBool_Check(a[6])) return not_here();
         const at::Tensor *q = tensor(a[0]), *pos = tensor(a[1]), *freq = tensor(a[2]), *axes = tensor(a[3]);
         const at::Tensor* k = a[4] == Py_None ? nullptr : tensor(a[4]);
         int dtype = 0;
@@ -287,7 +287,7 @@ PyObject* rotary(PyObject*, PyObject* const* a, Py_ssize_t n) {
                                 k != nullptr ? static_cast<int>(k->size(dim - 2)) : 0, static_cast<const int*>(pos->data_ptr()),
                                 static_cast<const double*>(freq->data_ptr()), static_cast<const int*>(axes->data_ptr()),
                                 static_cast<int>(T), static_cast<int>(A), static_cast<int>(F), static_cast<int>(D),
-                                PyObject_IsTrue(a[5]) == 1, PyObject_IsTrue(a[6]) == 1, dtype, stream_of(dev));
+                                a[5] == Py_True, a[6] == Py_True, dtype, stream_of(dev));
         if (rc != FA_OK) return PyLong_FromLong(rc);
         PyObject* y = THPVariable_Wrap(std::move(out[0]));
         return k == nullptr ? y : Py_BuildValue("(NN)", y, THPVariable_Wrap(std::move(out[1])));

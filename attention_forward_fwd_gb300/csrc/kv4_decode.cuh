@@ -1,5 +1,5 @@
 // kv4_decode.cuh -- attention of a few query rows over the quantised cache
-// (fa_kv4_attention for at most 16 query rows a K/V head: single tokens,
+// (fa_kv4_attention for at most 32 query rows a K/V head: single tokens,
 // drafted tokens; grouped heads share the K/V row, so the rows of a K/V head
 // are its group's heads times the call's tokens).
 //
@@ -84,8 +84,8 @@ struct Tile {
     static constexpr int kScales = kBlock * 2 * NG;
     static constexpr int kStage = 2 * (kCodes + kScales);
     // As many blocks in flight as leave room for three CTAs an SM (D <= 128; two
-    // above): a block's copies take about 2 us under load, whatever its size, and
-    // with two stages that was the time of a block.
+    // above).  A warp then waits some 20 cycles a block for its copies (131072 keys,
+    // D = 128); more stages took as long.
     static constexpr int kStages = NG <= 2 ? 6 : NG == 3 ? 4 : NG <= 6 ? 3 : 2;
     static constexpr int kRing = kWarps * kStages * kStage;
 };
@@ -104,6 +104,10 @@ constexpr int kClusterSmem = 8 * NT * (Tile<NG>::D * 4 + 8);
 template <int NG, int NT>
 constexpr int kDecodeSmem = Tile<NG>::kRing + kWarps * kPartFloats<NG, NT> * 4 + 2048;
 
+// The first key that a row at `pos` sees.  (pos is negative for rows in front of
+// a sequence, and the window may be any int: their difference need not fit one.)
+__device__ __forceinline__ int first_key(int pos, int window) { return window < 0 ? 0 : max(0, max(0, pos) - window); }
+
 // The rows of the call for a sequence as items: tiles x heads, each of `blocks` key blocks from key `first`.
 struct Work {
     int n, len, row0, tiles, items, blocks, first;
@@ -119,7 +123,7 @@ __device__ __forceinline__ Work work_of(const Cache& c, const Attend& a, int b, 
     w.tiles = (s.n * a.G + tile_rows - 1) / tile_rows;
     w.items = w.tiles * c.Hkv;
     w.first = 0;
-    if (s.n > 0 && a.window >= 0) w.first = max(0, s.len - s.n - a.window) / kBlock * kBlock;
+    if (s.n > 0) w.first = first_key(s.len - s.n, a.window) / kBlock * kBlock;
     w.blocks = s.n > 0 ? max(1, (max(0, s.len - w.first) + kBlock - 1) / kBlock) : 0;
     return w;
 }
@@ -532,12 +536,12 @@ __global__ void __launch_bounds__(kThreads, NG <= 4 && NT == 1 ? 3 : 2) decode_k
                 const int rr = t * 8 + 2 * cc + e;
                 const int pos = w.len - w.n + (tile * R + rr) / a.G;
                 hi_key[t][e] = rr < rows ? pos : 0x7fffffff;
-                lo_key[t][e] = rr < rows && a.window >= 0 ? max(0, pos - a.window) : 0;
+                lo_key[t][e] = rr < rows ? first_key(pos, a.window) : 0;
             }
         }
         // keys that every row of the tile sees
         const int all_hi = w.len - w.n + tile * R / a.G;
-        const int all_lo = a.window >= 0 ? max(0, w.len - w.n + (tile * R + rows - 1) / a.G - a.window) : 0;
+        const int all_lo = first_key(w.len - w.n + (tile * R + rows - 1) / a.G, a.window);
 
         float acc[NT][NG][2][4];
         float thr[NT][2], neg_ref[NT][2], l_sum[NT][2];   // raw score that moves the reference; -(m - kHead + E)

@@ -189,7 +189,7 @@ __global__ void __launch_bounds__(Prompt<NG>::kThreads, 1) prompt_kernel(Cache c
     // groups of keys that some row sees, and this split's share of them; the
     // last group's second tile is left out where no row sees it
     const int pos0 = w.len - w.n + tile * R / a.G, pos1 = w.len - w.n + (tile * R + rows - 1) / a.G;
-    const int g_lo = a.window >= 0 ? max(0, pos0 - a.window) / GK : 0;
+    const int g_lo = first_key(pos0, a.window) / GK;
     const int g_all = pos1 >= 0 ? pos1 / GK + 1 - g_lo : 0;
     const int gb = g_lo + static_cast<int>(static_cast<long long>(g_all) * split / splits);        // first group
     const int n_groups = g_lo + static_cast<int>(static_cast<long long>(g_all) * (split + 1) / splits) - gb;
@@ -427,7 +427,7 @@ __global__ void __launch_bounds__(Prompt<NG>::kThreads, 1) prompt_kernel(Cache c
         const int qi = rho / a.G, h = head * a.G + rho - qi * a.G;
         // rows past the last one see everything (their Q is 0), so that they need no mask
         const int pos = real ? w.len - w.n + qi : 0x7fffffff;
-        const int first = real && a.window >= 0 ? max(0, pos - a.window) : 0;
+        const int first = real ? first_key(pos, a.window) : 0;
         const uint32_t lane_off = static_cast<uint32_t>(32 * (warp & 3)) << 16;
         float f;   // z = S 2^Ek f
         {

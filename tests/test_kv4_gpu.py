@@ -631,3 +631,33 @@ def test_two_streams_at_once(fa):
         torch.cuda.synchronize()
         for (a, al), (b, bl) in zip(alone, got):
             assert torch.equal(a, b) and torch.equal(al, bl)
+
+
+@pytest.mark.parametrize("L", [512, 513, 544, 545, 1024, 1056, 1057, 2048, 2080, 2081, 4096, 4128, 4129])
+def test_contexts_around_the_cluster_sizes(fa, L):
+    """Tables that end where a cluster of 1, 2, 4 or 8 CTAs does, and just behind;
+    shorter sequences, of which some CTAs of the cluster get nothing."""
+    s = Setup([L, 40, 0, L - 33], 1, 64, 16, seed=L)
+    run_attention(fa, s, "bf16", 2, [1] * 4, packed=False)
+    run_attention(fa, s, "f16", 3, [4, 0, 1, 4], packed=True, window=L // 3)
+
+
+@pytest.mark.parametrize("native", [True, False])
+@pytest.mark.parametrize("n", [4, 70])
+def test_windows_of_any_int(fa, monkeypatch, native, n):
+    """A window as far as an int goes, or farther, bounds nothing; rows before the
+    first token stand at negative positions."""
+    import torch
+    from attention_forward_fwd_gb300 import cache
+    if not native:
+        monkeypatch.setattr(cache, "_native", None)
+    s = Setup([150, 3, 0, 1], 2, 64, 16, seed=n)
+    c = s.cuda()
+    q = dev(to16(s.r.standard_normal((4, n, 4, 64)), "bf16"), "bf16")
+    o, lse = fa.kv4_attention(q, **c)
+    for window in (149, 2**31 - 1, 2**31, 2**32, 2**40):
+        p, l2 = fa.kv4_attention(q, **c, window_left=window)
+        assert torch.equal(o, p) and torch.equal(lse, l2)
+    for window in (-2, -2**31, -2**32, -2**33 + 5):
+        with pytest.raises(fa.FaError):
+            fa.kv4_attention(q, **c, window_left=window)
