@@ -450,15 +450,15 @@ int fa_rotary(const void* X, const long long* x_strides, void* Y, const long lon
     p.F = n_freq;
     p.D = D;
     p.inverse = inverse != 0;
-    // enough tokens a CTA for every thread's units in flight, while the CTAs
+    // enough tokens a CTA to give every thread units, while the CTAs
     // still fill the GPU (152 SMs, 8 CTAs each)
     const int vec = wide ? 8 : 1;
-    const int per_token = (H + H2) * (n_freq / vec + (D - 2 * n_freq + 2 * vec - 1) / (2 * vec));
-    int tokens = rot::kThreads * rot::kUnroll / per_token;
+    const int per_token = (H + H2 + rot::kUnroll - 1) / rot::kUnroll * (n_freq / vec + (D - 2 * n_freq + 2 * vec - 1) / (2 * vec));
+    int tokens = rot::kThreads / per_token;
     tokens = std::min(tokens, T / (152 * 8));
     p.tokens = std::max(1, std::min(tokens, rot::kMaxTokens));
     const unsigned blocks = static_cast<unsigned>((static_cast<long long>(T) + p.tokens - 1) / p.tokens);
-    const size_t smem = static_cast<size_t>(p.tokens) * n_freq * sizeof(float2);
+    const size_t smem = static_cast<size_t>(p.tokens + 1) * n_freq * sizeof(float2);
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     const bool bf16 = dtype == FA_BF16;
     if (wide) return interleaved ? rotate<8, true>(p, bf16, blocks, smem, st) : rotate<8, false>(p, bf16, blocks, smem, st);
