@@ -208,6 +208,10 @@ struct Words {
     __device__ __forceinline__ void set(int i, uint32_t w) {   // w < 2^16
         u[i / 2] = (i & 1) ? (u[i / 2] & 0xffffu) | (w << 16) : (u[i / 2] & 0xffff0000u) | w;
     }
+    // word i from the low or the high half of w
+    __device__ __forceinline__ void set_half(int i, uint32_t w, bool high) {
+        u[i / 2] = __byte_perm(u[i / 2], w, (i & 1) ? (high ? 0x7610u : 0x5410u) : (high ? 0x3276u : 0x3254u));
+    }
     // word i as a bfloat16
     __device__ __forceinline__ float bf16(int i) const {
         return __uint_as_float((i & 1) ? u[i / 2] & 0xffff0000u : u[i / 2] << 16);
@@ -312,9 +316,10 @@ __device__ __forceinline__ uint32_t group_scale(const uint32_t* x, int sub) {
 // Exactness: rint(x / s) is taken of x times an approximate 1 / s, which is off
 // by less than 2^-20.  x has at most 11 significant bits and s at most 8, so x / s is
 // either a tie k + 1/2 or at least 2^-13 away from one; rounding the product
-// to multiples of 2^-14 first restores the ties and moves nothing across one.
-// x / s is at least -8 (1 + 2^-8), which rounds to -8: only 7 needs a clamp, but for
-// subnormal scales, whose own rounding is coarser.
+// to multiples of 2^-14 first (768 is added to it, in the same instruction)
+// restores the ties and moves nothing across one.  x / s is at least -8 (1 + 2^-8),
+// which rounds to -8: only 7 needs a clamp, but for subnormal scales, whose own
+// rounding is coarser.
 //
 // Bound by instructions as much as by DRAM: 14 a value are what the measured
 // bandwidth leaves.  The loop over the rows is not unrolled, for the
@@ -378,40 +383,42 @@ __global__ void __launch_bounds__(kRowThreads) write_kernel(Cache c, RowIo io) {
             float inv;
             asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
             if (tiny) inv = 0.f;
-            float u[8];
+            float2 t[4];   // 768 and x / s, to multiples of 2^-14
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float2 f = to_f32x2<BF16>(e[j]);
-                u[2 * j] = f.x * inv;
-                u[2 * j + 1] = f.y * inv;
-            }
+            for (int j = 0; j < 4; ++j) t[j] = __ffma2_rn(to_f32x2<BF16>(e[j]), make_float2(inv, inv), make_float2(768.f, 768.f));
             if (__any_sync(0xffffffffu, tiny && sb != 0)) {
                 const float lifted = __frcp_rn(s * 7.92281625e28f);   // 2^96
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float2 f = to_f32x2<BF16>(e[j / 2]);
-                    if (tiny && sb != 0) u[j] = fmaxf(((j & 1) ? f.y : f.x) * 7.92281625e28f * lifted, -8.f);
+                for (int j = 0; j < 4; ++j) {
+                    const float2 f = to_f32x2<BF16>(e[j]);
+                    if (tiny && sb != 0)
+                        t[j] = make_float2(__fadd_rn(fmaxf(f.x * 7.92281625e28f * lifted, -8.f), 768.f),
+                                           __fadd_rn(fmaxf(f.y * 7.92281625e28f * lifted, -8.f), 768.f));
                 }
             }
-            int m[8];
-            float q[8];
+            uint32_t pair[4];   // codes 2 j and 2 j + 1, 16 bits each
+            uint32_t o[4];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float w = fminf(__fadd_rn(__fadd_rn(u[j], 768.f), -768.f), 7.f);   // to multiples of 2^-14
-                const float r = __fadd_rn(w, 12582920.f);       // 8 more than the nearest integer, ties to even
-                m[j] = __float_as_int(r);
-                if constexpr (VALUES) q[j] = __fadd_rn(r, -12582920.f) * s;
+            for (int j = 0; j < 4; ++j) {
+                // 3 2^22 + 8 and the nearest integer, ties to even: the low bits are the code, or 16
+                float2 r = __fadd2_rn(t[j], make_float2(12582152.f, 12582152.f));
+                if constexpr (VALUES) {
+                    r = make_float2(fminf(r.x, 12582927.f), fminf(r.y, 12582927.f));
+                    const float2 n = __fadd2_rn(r, make_float2(-12582920.f, -12582920.f));
+                    o[j] = pack16<BF16>(n.x * s, n.y * s);
+                }
+                pair[j] = __byte_perm(__float_as_uint(r.x), __float_as_uint(r.y), 0x5410);
+                if constexpr (!VALUES) pair[j] = __vminu2(pair[j], 0x000f000fu);
             }
-            // the integers sit in the low bits; what is above them leaves the low 16 bits of the sums
-            uint32_t w0 = static_cast<uint32_t>(m[0] + m[1] * 16 + m[2] * 256 + m[3] * 4096) & 0xffffu;
-            uint32_t w1 = static_cast<uint32_t>(m[4] + m[5] * 16 + m[6] * 256 + m[7] * 4096) & 0xffffu;
-            if (sb == 0x7fc0u) w0 = w1 = 0x8888u;
-            codes.set(g, w0);          // r = 2 c
-            codes.set(NG + g, w1);     // r = 2 c + 1
+            // a code a byte; then two in bytes 0 and 2
+            const uint32_t a0 = __byte_perm(pair[0], pair[1], 0x6420), a1 = __byte_perm(pair[2], pair[3], 0x6420);
+            const uint32_t b0 = a0 + (a0 >> 4), b1 = a1 + (a1 >> 4);
+            uint32_t both = __byte_perm(b0, b1, 0x6420);       // r = 2 c below r = 2 c + 1
+            if (sb == 0x7fc0u) both = 0x88888888u;
+            codes.set_half(g, both, false);
+            codes.set_half(NG + g, both, true);
             scales.set(g, sb);
-            if constexpr (VALUES)
-                x[g] = make_uint4(pack16<BF16>(q[0], q[1]), pack16<BF16>(q[2], q[3]), pack16<BF16>(q[4], q[5]),
-                                  pack16<BF16>(q[6], q[7]));
+            if constexpr (VALUES) x[g] = make_uint4(o[0], o[1], o[2], o[3]);
         }
         if (place == kRowOk) {
             const long long row = (page * 2 * c.Hkv + y) * c.P + at;   // K's heads, then V's
