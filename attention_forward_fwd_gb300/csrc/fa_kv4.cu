@@ -81,7 +81,7 @@ template <int NG, int LANES>
 unsigned row_blocks(const kv4::Cache& c, int* per) {
     constexpr int TOK = 32 / LANES;
     const long long groups = (static_cast<long long>(c.total) + TOK - 1) / TOK, rows = 2LL * c.Hkv;
-    *per = static_cast<int>(std::max<long long>(1, std::min<long long>(kv4::kRows<NG>, groups * rows / (152 * 16))));
+    *per = static_cast<int>(std::max<long long>(1, std::min<long long>(kv4::kRows<NG, LANES>, groups * rows / (152 * 16))));
     const long long warps = groups * ((rows + *per - 1) / *per);
     const long long blocks = (warps + kv4::kRowThreads / 32 - 1) / (kv4::kRowThreads / 32);
     return blocks > 0x7fffffffLL ? 0u : static_cast<unsigned>(blocks);

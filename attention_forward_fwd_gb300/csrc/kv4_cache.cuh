@@ -237,17 +237,22 @@ struct RowIo {
 };
 
 // Both kernels: a warp takes 32 / LANES tokens, LANES neighbouring threads
-// each, and up to kRows<NG> of their rows (K or V of a head) one after the other: where
+// each, and up to kRows<NG, LANES> of their rows (K or V of a head) one after the other: where
 // a token lies is found once for all of them, while the first row's loads are
 // under way.  The rows of an access are tokens of the same head, so that their
 // scales fill whole sectors.
 //  * read: 8 threads a row, thread r has elements 4 r .. 4 r + 3 of every group.
 //  * write: 4 threads a row, thread c has elements 8 c .. 8 c + 7, because the search
 //    for a group's extreme is paid once a thread and group, whatever they hold.
-constexpr int kRowThreads = 256;
-template <int NG>
-constexpr int kRows = NG <= 2 ? 8 : NG <= 4 ? 4 : 2;
+// CTAs of 128 threads, not 256: these have no more in common, and smaller ones follow one
+// another more evenly (D = 128, prompts of 37000 tokens, 8 heads: write 69.7 -> 61.7 us,
+// 84 % of the copy bandwidth; 65536 tokens of 8 rows of 64: 27.6 -> 24.2).
+constexpr int kRowThreads = 128;
 constexpr int kWriteLanes = 4, kReadLanes = 8;
+// A write holds one row and the next; a read all of them, which pays for longer
+// (D = 128: read of 75000 tokens 69.7 us with 4 rows, 67.5 with 8; the write above 61.7, 63.5).
+template <int NG, int LANES>
+constexpr int kRows = (NG <= 2 ? 8 : NG <= 4 ? 4 : 2) * (LANES == kReadLanes ? 2 : 1);
 
 // Which rows a warp takes.
 struct RowShare {
@@ -467,7 +472,7 @@ __device__ __forceinline__ uint32_t code_values(uint32_t pair, uint32_t s2) {
 
 template <int NG, bool BF16>
 __global__ void __launch_bounds__(kRowThreads) read_kernel(Cache c, RowIo io) {
-    constexpr int D = NG * kGroup, N = kRows<NG>;
+    constexpr int D = NG * kGroup, N = kRows<NG, kReadLanes>;
     if (blockIdx.x == 0) check_sequences(c);
     RowShare own;
     if (!row_share<kReadLanes>(c, io.per, &own) || own.t >= c.total) return;
