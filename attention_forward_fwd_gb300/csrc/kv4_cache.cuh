@@ -250,7 +250,7 @@ struct RowIo {
 constexpr int kRowThreads = 128;
 constexpr int kWriteLanes = 4, kReadLanes = 8;
 // A write holds one row and the next; a read all of them, which pays for longer
-// (D = 128: read of 75000 tokens 69.7 us with 4 rows, 67.5 with 8; the write above 61.7, 63.5).
+// (D = 128: read of 80000 tokens 69.7 us with 4 rows, 67.5 with 8; the write above 61.7, 63.5).
 template <int NG, int LANES>
 constexpr int kRows = (NG <= 2 ? 8 : NG <= 4 ? 4 : 2) * (LANES == kReadLanes ? 2 : 1);
 
@@ -326,8 +326,8 @@ __device__ __forceinline__ uint32_t group_scale(const uint32_t* x, int sub) {
 // which rounds to -8: only 7 needs a clamp, but for subnormal scales, whose own
 // rounding is coarser.
 //
-// Bound by instructions as much as by DRAM: 14 a value are what the measured
-// bandwidth leaves.  The loop over the rows is not unrolled, for the
+// Bound by DRAM at D = 128 when the values come back, by instructions where rows are
+// narrow and they do not (figures above).  The loop over the rows is not unrolled, for the
 // instruction cache's sake; the next row is loaded ahead.
 template <int NG, bool BF16, bool VALUES>
 __global__ void __launch_bounds__(kRowThreads) write_kernel(Cache c, RowIo io) {

@@ -347,7 +347,7 @@ int fa_fwd_splitkv_static(const void* Q, const void* K, const void* V, void* O, 
  *
  * D is a multiple of 32 up to 256, page_size a multiple of 16; codes and
  * scales are 16-byte aligned; pages * page_size and the rows of a call are
- * numbered with an int.  Errors: FA_ERR_INVALID_ARG for NULL pointers, sizes
+ * numbered with an int (max_pages * page_size: 4096 less).  Errors: FA_ERR_INVALID_ARG for NULL pointers, sizes
  * below 1, or an unknown dtype; FA_ERR_UNSUPPORTED for the limits of this paragraph.
  */
 typedef struct {
@@ -386,12 +386,17 @@ int fa_kv4_read(const fa_kv4_cache_t* cache, void* K, void* V, int dtype, fa_str
  * .. p (window_left = -1: from 0).  Query head h uses K/V head
  * h / (H / H_kv).  Q: 16-bit [.., H, D] with strides (batch, row, head) in
  * elements, multiples of 8; O: contiguous, Q's type; LSE: fp32 [B, H, max_seqlen], or
- * [H, total] for packed tensors, or NULL.  The keys are split over CTAs
- * and the parts joined by a second kernel on the same stream, through
- * `workspace` (16-byte aligned, of fa_kv4_attention_workspace_size bytes for
- * the same cache, H and dtype on the same device; no initialisation).  Calls
- * that share a workspace must be ordered on one stream.  A NaN in Q or in a
- * visible key makes its row NaN, one in a visible value its group's elements.
+ * [H, total] for packed tensors, or NULL; neither may overlap Q.
+ * `workspace`: 16-byte aligned, of fa_kv4_attention_workspace_size bytes for
+ * the same cache, H and dtype on the same device; no initialisation.  It holds
+ * the parts of results whose keys several CTAs share, which a second kernel on
+ * the same stream joins; calls that need none (short tables; prompts that fill the GPU
+ * with whole rows) have size 0 and take NULL.  Calls that share a workspace
+ * must be ordered on one stream.  A NaN in Q or in a visible key makes its row
+ * NaN, one in a visible value its group's elements; what masked or absent keys
+ * hold does not matter.  Up to 32 query rows a K/V head (rows of the call times
+ * H / H_kv) a streaming kernel runs, above it one on the tcgen05 tensor cores;
+ * both give the same results up to rounding (2^-12 of the largest weights, and O's own).
  * Errors besides the cache's: FA_ERR_INVALID_ARG for H < 1, H not a multiple
  * of H_kv, window_left < -1, scale not finite or <= 0, a missing or too small
  * workspace.
