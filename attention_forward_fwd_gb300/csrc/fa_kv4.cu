@@ -456,7 +456,7 @@ int fa_rotary(const void* X, const long long* x_strides, void* Y, const long lon
     const int per_token = (H + H2 + rot::kUnroll - 1) / rot::kUnroll * (n_freq / vec + (D - 2 * n_freq + 2 * vec - 1) / (2 * vec));
     int tokens = rot::kThreads / per_token;
     tokens = std::min(tokens, T / (152 * 8));
-    p.tokens = std::max(1, std::min(tokens, rot::kMaxTokens));
+    p.tokens = std::max(1, std::min(tokens, rot::kMaxAngles / n_freq));
     const unsigned blocks = static_cast<unsigned>((static_cast<long long>(T) + p.tokens - 1) / p.tokens);
     const size_t smem = static_cast<size_t>(p.tokens + 1) * n_freq * sizeof(float2);
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);

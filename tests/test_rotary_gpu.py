@@ -151,3 +151,23 @@ def test_captured(fa):
         pos.fill_(p)
         g.replay()
         assert torch.equal(y, fa.rotary(x, pos, freq, axes))
+
+
+@pytest.mark.parametrize("T,H,Hk,D,F", [(200000, 1, 0, 16, 8), (90001, 2, 1, 64, 32), (30011, 1, 1, 256, 128),
+                                        (25000, 1, 0, 40, 13), (5000, 3, 6, 96, 40)])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_many_tokens_of_few_heads(fa, T, H, Hk, D, F, interleaved):
+    """However many tokens share a CTA, each is turned as in a call of its own few."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(T)
+    q = torch.randn(T, H, D, generator=g, device="cuda").bfloat16()
+    k = torch.randn(T, Hk, D, generator=g, device="cuda").bfloat16() if Hk else None
+    pos = torch.randint(-1000, 1 << 20, (T, 2), generator=g, device="cuda", dtype=torch.int32)
+    freq, axes = fa.rotary_frequencies(2 * F, (F - F // 3, F // 3), interleave_axes=True)
+    whole = fa.rotary(q, pos, freq, axes, k=k, interleaved=interleaved)
+    whole = whole if Hk else (whole,)
+    for lo, hi in ((0, 150), (T // 2 - 3, T // 2 + 140), (T - 131, T)):
+        some = fa.rotary(q[lo:hi], pos[lo:hi], freq, axes, k=k[lo:hi] if Hk else None, interleaved=interleaved)
+        for x, y in zip(whole, some if Hk else (some,)):
+            assert torch.equal(x[lo:hi], y)
+    assert fa.fa_device_status() == 0
