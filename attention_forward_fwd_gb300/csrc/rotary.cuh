@@ -27,10 +27,10 @@ namespace rot {
 constexpr int kThreads = 256;
 constexpr int kUnroll = 4;          // units a thread has in flight
 constexpr int kMaxFreqs = 128;
-// Angles of a CTA's tokens (24 KB).  With few heads a CTA needs many tokens to have
+// Angles of a CTA's tokens (32 KB).  With few heads a CTA needs many tokens to have
 // work for its threads: 280582 tokens of 4 heads of 64 take 101 us, with 512 angles 134
 // (there the angles, one for 4 pairs, are what it spends its time on).
-constexpr int kMaxAngles = 3072;
+constexpr int kMaxAngles = 4096;
 constexpr int kStatusBadAxis = 8;
 
 struct Rotary {
